@@ -10,6 +10,9 @@ fallback, and a missing library raises at the first call.
                     "SPICY-KV" node statistics (mass, mean key/value, variance)
   decode_attn(...)  "SPICY-KV" section 2 decode logit
                     q.k/sqrt(d) + ln m + |q|^2 sigma^2/(2d) with online softmax
+
+Tokens that are not coarsened live in a TokenCache (token_cache.py): cache_append writes them,
+cache_read hands a range to coarsen, paged_attn attends over them and joins decode_attn's result.
 """
 from __future__ import annotations
 
@@ -19,11 +22,14 @@ import math
 import torch
 
 from . import _lib
-from ._lib import PAGE_NODES, SkvError
+from ._lib import CACHE_PAGE_TOKENS, PAGE_NODES, SkvError
+from .token_cache import (TokenCache, cache_append, cache_page_bytes, cache_read, paged_attn,
+                          paged_attn_workspace_bytes, token_pages_for)
 
 __all__ = ["NodePool", "coarsen", "decode_attn", "coarsen_workspace_bytes", "decode_workspace_bytes",
            "workspace_error", "projection_matrix", "entries_bound", "pages_for", "page_bytes", "read_entries",
-           "SkvError", "PAGE_NODES", "library_path"]
+           "SkvError", "PAGE_NODES", "library_path", "TokenCache", "cache_append", "cache_read", "paged_attn",
+           "paged_attn_workspace_bytes", "cache_page_bytes", "token_pages_for", "CACHE_PAGE_TOKENS"]
 
 
 def library_path() -> str:

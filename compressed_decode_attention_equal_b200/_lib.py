@@ -37,6 +37,20 @@ class SkvDecodeOptions(ctypes.Structure):
     _fields_ = [("closure", ctypes.c_int32), ("reserved", ctypes.c_int32 * 7)]
 
 
+CACHE_PAGE_TOKENS, CACHE_GROUP_TOKENS = 64, 16
+SKV_CACHE_RAW, SKV_CACHE_E4M3 = 0, 1
+
+
+class SkvTokenCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64)]
+
+
+class SkvPagedAttnOptions(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("reserved", ctypes.c_int32 * 4), ("first", ctypes.c_void_p), ("slopes", ctypes.c_void_p),
+                ("prior_out", ctypes.c_void_p), ("prior_lse", ctypes.c_void_p)]
+
+
 class SkvError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -47,6 +61,8 @@ class SkvError(RuntimeError):
 EXPORTS = ("skv_status_string", "skv_abi_version", "skv_page_bytes", "skv_page_bytes_ex", "skv_projection_matrix",
            "skv_coarsen_workspace_bytes",
            "skv_coarsen", "skv_coarsen_ex", "skv_decode_workspace_bytes", "skv_decode_attn", "skv_decode_attn_ex", "skv_decode_attn_noalloc",
+           "skv_cache_page_bytes", "skv_cache_append", "skv_cache_read",
+           "skv_paged_attn_workspace_bytes", "skv_paged_attn",
            "skv_stream_state_bytes", "skv_stream_init", "skv_stream_append",
            "skv_workspace_error", "skv_wait_selftest")
 
@@ -102,6 +118,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.skv_decode_attn_noalloc.argtypes = [vp, i32, i32, i32, i32, i32, i32, ctypes.POINTER(SkvNodePool), vp,
                                             i32, vp, vp, vp, vp]
     lib.skv_decode_attn_noalloc.restype = i32
+    pcache = ctypes.POINTER(SkvTokenCache)
+    lib.skv_cache_page_bytes.argtypes = [i32, i32, i32, i32]
+    lib.skv_cache_page_bytes.restype = sz
+    lib.skv_cache_append.argtypes = [vp, vp, i32, i64, i64, i64, i64, i32, i32, i32, i32, vp, i32, pcache, vp, i32,
+                                     vp, vp, vp, sz, vp]
+    lib.skv_cache_append.restype = i32
+    lib.skv_cache_read.argtypes = [pcache, i32, i32, i32, i32, i32, pi32, pi32, vp, i32, vp, vp, vp, sz, vp]
+    lib.skv_cache_read.restype = i32
+    lib.skv_paged_attn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.skv_paged_attn_workspace_bytes.restype = sz
+    lib.skv_paged_attn.argtypes = [vp, i32, i64, i64, i64, i32, i32, i32, i32, i32, i32, pcache, vp, i32, vp, vp, vp,
+                                   vp, sz, ctypes.POINTER(SkvPagedAttnOptions), vp]
+    lib.skv_paged_attn.restype = i32
     lib.skv_workspace_error.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.skv_workspace_error.restype = i32
     lib.skv_wait_selftest.argtypes = [vp, sz, ctypes.c_uint32, vp]

@@ -393,6 +393,129 @@ skv_status skv_decode_attn_noalloc(const void *q, skv_dtype dtype, int B, int R,
                                    const int32_t *lens, void *out, float *lse, void *stream);
 
 /*
+ * The exact-token cache: keys and values of tokens that are not (or not yet) coarsened, in pages,
+ * with the operators that write it, read it back and attend over it. (The sources describe no such
+ * cache; it holds the history that skv_coarsen takes, and the tokens behind a coarsened prefix.)
+ *
+ * A page holds SKV_CACHE_PAGE_TOKENS = 64 tokens of one sequence for all its Hkv heads, as
+ * [Hkv][4 groups][group]; a group holds 16 tokens of one head:
+ *   SKV_CACHE_RAW : keys [16][d], values [16][d] in the inputs' dtype
+ *   SKV_CACHE_E4M3: key codes [16][d], value codes [16][d] (e4m3, one byte each), then one byte
+ *     e + 127 for each key [16] and each value [16]; the value held is code * 2^e. For a vector x
+ *     with a = max |x_i| over its finite elements, e is the smallest integer with a <= 448 * 2^e,
+ *     limited to -100 .. 119 (0 for a = 0), and code_i = x_i 2^-e rounded once to e4m3 (nearest
+ *     even, at most 2^-4 relative, saturating at 448: infinities are held as +-448 * 2^e; NaN stays
+ *     NaN). Reading back into either dtype is exact.
+ * Inside the key and value blocks the 16-byte chunk c of slot n is stored at chunk
+ * c ^ (((n & 6) ^ ((n & 1) << 2)) & (chunks - 1)), chunks = 16-byte chunks per vector.
+ * page_table : [B][max_pages] int32 page ids; position t of sequence b lies in page
+ *              page_table[b][t / 64], slot t % 64. Sequences may share pages that none appends to.
+ * lens       : [B] int32 tokens held.
+ * The pages pointer must be 16-byte aligned; num_pages at most INT32_MAX, max_pages * 64 at most
+ * 2^30, Hkv at most 65,535. Slots behind a sequence's last token are never read into a result: they
+ * may hold anything.
+ */
+#define SKV_CACHE_PAGE_TOKENS 64
+
+typedef enum { SKV_CACHE_RAW = 0, SKV_CACHE_E4M3 = 1 } skv_cache_format;
+
+typedef struct {
+    void *pages;       /* [num_pages][skv_cache_page_bytes(dtype, format, Hkv, d)] (device) */
+    int64_t num_pages; /* capacity, in pages */
+} skv_token_cache;
+
+/* Bytes of one page (0 for unsupported arguments). */
+size_t skv_cache_page_bytes(skv_dtype dtype, skv_cache_format format, int Hkv, int d);
+
+/*
+ * Append tokens, quantising them on the way (SKV_CACHE_E4M3).
+ *
+ * k, v      : [n_tokens][Hkv][d] in dtype, d contiguous; token and head strides in elements (slices
+ *             of a fused projection need no copy). 16-byte aligned, strides multiples of 16 bytes.
+ * cu_new    : [B + 1] int32 device: rows cu_new[b] .. cu_new[b + 1] - 1 are sequence b's new tokens
+ *             (0 <= cu_new[b] <= cu_new[b + 1] <= n_tokens). Rows outside are ignored. NULL: every
+ *             sequence gets n_tokens / B tokens (n_tokens a multiple of B).
+ * lens      : [B] int32 device, tokens held before: new token i goes to position lens[b] + i, whose
+ *             page the page table must already name.
+ * new_lens  : [B] int32 device output, lens + the new tokens. May be lens itself (updated in place).
+ * workspace : >= 256 bytes, zero-filled before its first use: error flags and a counter that every
+ *             call returns to zero.
+ * One launch, graph-capturable. Device-detected, the offending tokens skipped: a page id outside the
+ * cache; lens below zero or above max_pages * 64 (the sequence is left as it is); tokens behind
+ * that capacity (new_lens is then the capacity); a cu_new that does not run upwards within n_tokens
+ * (that sequence gets none). Errors: SKV_ERR_INVALID_ARG, SKV_ERR_UNSUPPORTED (dtype, d, more than
+ * INT32_MAX token-heads), SKV_ERR_WORKSPACE, SKV_ERR_CUDA.
+ */
+skv_status skv_cache_append(const void *k, const void *v, skv_dtype dtype, int64_t k_token_stride,
+                            int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, int B, int Hkv, int d,
+                            int n_tokens, const int32_t *cu_new, skv_cache_format format, const skv_token_cache *cache,
+                            const int32_t *page_table, int max_pages, const int32_t *lens, int32_t *new_lens,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Read positions [first_b, first_b + T_b) of every sequence back into the packed layout that
+ * skv_coarsen takes: sequence b a contiguous [Hkv][T_b][d] block of k and v in dtype.
+ * first_host, T_host: [B] host (first_b + T_b <= max_pages * 64; the positions must have been
+ * appended). A page id outside the cache gives zeros and sets the device flag. workspace: >= 256
+ * bytes (error flags). Errors as skv_cache_append.
+ */
+skv_status skv_cache_read(const skv_token_cache *cache, skv_dtype dtype, skv_cache_format format, int B, int Hkv, int d,
+                          const int32_t *first_host, const int32_t *T_host, const int32_t *page_table, int max_pages,
+                          void *k, void *v, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Options of skv_paged_attn; all zero (or NULL) are the defaults.
+ * scale     : logit scale; 0 stands for 1 / sqrt(d).
+ * softcap   : c > 0: s becomes c tanh(s / c).
+ * window    : w > 0: only the last w tokens are seen.
+ * first     : [B] int32 device: only positions >= first[b] are seen (below 0 reads as 0; at or above
+ *             lens[b] the sequence has no key).
+ * slopes    : [Hq] fp32 device: s -= slope * (lens[b] - 1 - j), after the cap.
+ * prior_out, prior_lse: another attention of the same queries over other keys, as skv_decode_attn
+ *             or this call return it ([B][R][Hq][d] in dtype, [B][R][Hq] fp32): the outputs are then
+ *             those of one attention over both sets of keys. prior_out may be out itself; prior_lse may
+ *             not overlap lse. A prior_lse of -inf stands for no keys (its prior_out is not read).
+ * reserved  : must be zero.
+ */
+typedef struct {
+    float scale;
+    float softcap;
+    int32_t window;
+    int32_t reserved[4];
+    const int32_t *first;
+    const float *slopes;
+    const void *prior_out;
+    const float *prior_lse;
+} skv_paged_attn_options;
+
+/* Bytes of device workspace skv_paged_attn needs (0 on invalid arguments). Calls of any shape that
+ * need no more may share it (not with skv_decode_attn), ordered on one stream. */
+size_t skv_paged_attn_workspace_bytes(int B, int R, int Hq, int Hkv, int d, int max_pages);
+
+/*
+ * Attention of the new token over the exact-token cache.
+ *
+ * q     : R query rows per sequence, q[b][r][hq] at element b q_seq_stride + r q_row_stride + hq
+ *         q_head_stride, d contiguous, in dtype; 16-byte aligned, strides multiples of 16 bytes. The
+ *         rows are independent (as skv_decode_attn's): each stands at the last position lens[b] - 1
+ *         and sees every key there is. Query head hq reads KV head hq / (Hq / Hkv).
+ * s_j = scale q.k_j (capped, biased) over the keys j in [max(first, lens - window), lens);
+ * out = softmax(s) V ([B][R][Hq][d] in dtype), lse = ln sum exp(s_j) ([B][R][Hq] fp32). A row that
+ * sees no key gives out = 0, lse = -inf (joined with a prior: the prior). NaN in a key or value that
+ * is seen gives NaN; what is not seen never enters.
+ * workspace : skv_paged_attn_workspace_bytes bytes, 256-byte aligned, zero-filled before its first use.
+ * The keys are split over the whole GPU and joined in a fixed order: equal inputs give equal bits.
+ * One launch, graph-capturable. Device-detected: page ids outside the cache (those tokens are skipped)
+ * and lens outside 0 .. max_pages * 64 (clamped) set the device flag. Errors: SKV_ERR_INVALID_ARG,
+ * SKV_ERR_UNSUPPORTED (dtype, d, Hq % Hkv, sizes), SKV_ERR_WORKSPACE, SKV_ERR_CUDA.
+ */
+skv_status skv_paged_attn(const void *q, skv_dtype dtype, int64_t q_seq_stride, int64_t q_row_stride,
+                          int64_t q_head_stride, int B, int R, int Hq, int Hkv, int d, skv_cache_format format,
+                          const skv_token_cache *cache, const int32_t *page_table, int max_pages, const int32_t *lens,
+                          void *out, float *lse, void *workspace, size_t ws_bytes,
+                          const skv_paged_attn_options *options, void *stream);
+
+/*
  * Check of the device error path that a stuck pipeline takes. Every wait of
  * the library's kernels on an mbarrier (a copy landing, a stage being freed)
  * polls at most 2^20 times; when the polls run out the kernel raises the
