@@ -224,6 +224,468 @@ __global__ void __launch_bounds__(kSimpleThreads) k_paged_f32(const PagedArgs a)
     }
 }
 
+// ---------------------------------------------------------------------------
+// bf16 queries: tensor cores
+// ---------------------------------------------------------------------------
+// Shared memory of k_paged_mma<E4M3, D, NT, W, S>: per warp a ring of S token groups, each one bulk
+// copy; the pass's query rows; the warps' outputs at the end of a piece.
+template <bool E4M3, int D, int NT, int W, int S>
+struct MmaSmem {
+    using G = CacheGeom<__nv_bfloat16, E4M3, D>;
+    static constexpr int kStage = (G::kGroup + 127) / 128 * 128;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kQRow = 2 * D + 8;      // bytes of a query row: 8 more than 2 D against bank conflicts
+    static constexpr int kMerge = 33;            // words per accumulator element of a warp's 32 lanes
+    alignas(128) uint8_t ring[W][S][kStage];
+    float o[W][4 * (D / 16)][kMerge];            // one tile of 8 rows of all warps
+    alignas(16) uint8_t q[kRows][kQRow];
+    float qfac[kRows], slope[kRows];
+    float m[W][kRows], l[W][kRows];
+    alignas(8) uint64_t full[W][S];
+    PagedSched sched;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool E4M3>
+__device__ __forceinline__ void mma_tile(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (E4M3) mma_f16(c, a0, a1, a2, a3, b0, b1);
+    else mma_bf16(c, a0, a1, a2, a3, b0, b1);
+}
+
+__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w)); }
+__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16)); }
+__device__ __forceinline__ uint32_t word(const uint4 &u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The token groups that one warp of a CTA takes, in order, over all pieces of the CTA's range: what
+// runs ahead of the computation to issue the copies. The page id of the group that comes next is
+// loaded one step before it is needed.
+template <int W>
+struct Feeder {
+    PagedWalk walk;
+    PagedPiece p;
+    int g, g_end, page;
+    bool live;
+
+    __device__ __forceinline__ void settle(const PagedArgs &a, const PagedSched &s, int warp) {
+        while (g >= g_end) {
+            if (!walk.next(a, s, &p)) {
+                live = false;
+                return;
+            }
+            const int lo = s.lo[p.b], hi = s.hi[p.b], g0 = lo / kGroupTokens;
+            g = g0 + p.r0 * W + warp;
+            g_end = hi > lo ? min((hi + kGroupTokens - 1) / kGroupTokens, g0 + p.r1 * W) : 0;
+        }
+        page = ld_global_s32(a.page_table + static_cast<int64_t>(p.b) * a.max_pages + g / kPageGroups);
+    }
+    __device__ __forceinline__ void begin(const PagedArgs &a, const PagedSched &s, int warp) {
+        walk.begin(a, s);
+        g = g_end = 0;
+        live = true;
+        settle(a, s, warp);
+    }
+    __device__ __forceinline__ void step(const PagedArgs &a, const PagedSched &s, int warp) {
+        g += W;
+        settle(a, s, warp);
+    }
+};
+
+// k_paged_mma (bf16 queries): mma.sync m16n8k16 with the tokens as M and 8 NT query rows as N, so that
+// a group of up to 8 query heads reads every key once and the logits' accumulators, after one 8x8
+// transpose per tile, are the second product's operand. HBM bounds it: a key and value are 258
+// (e4m3) or 512 (raw) bytes at d = 128 and 4 d flops per query row, ~10 flops per byte at 7 rows,
+// a tenth of what even this older matrix path does in that time; tcgen05 would need the
+// converted keys stored to shared or tensor memory again (its fp16 operand cannot be an e4m3 tile) and a
+// round trip of the scores through tensor memory per tile. So each warp works alone: it takes every W-th
+// token group of a piece, one bulk copy per group into a private ring, S groups ahead across piece ends,
+// and meets the other warps only at the end of a piece.
+//   Keys: the contraction order over d is free as long as keys and queries agree; a lane's 16
+//   bytes of a key row serve several steps, so that a group's keys are 4 (e4m3) or 8 (raw) 16-byte loads.
+//   Values: transposed on load by byte permutes of neighbouring tokens' words.
+//   e4m3: codes go to fp16 (exact); a query row is scaled by a power of two into fp16's range, exactly;
+//   the key's scale multiplies the logit, the value's exponent is added to the base-2 logit before the
+//   maximum is taken, so that the fp16 weight 2^(s + ve - max) holds the value's scale too, and the
+//   partition sums 2^(s + ve - max) 2^-ve.
+//   Weights are rounded to the matrix type (fp16 2^-11, bf16 2^-8 relative): the second product runs on
+//   16-bit operands, and the partition keeps the fp32 weights. Sums and maxima are fp32. The reference maximum
+//   moves only when a logit exceeds it by 2^8, so that the rescale of O runs rarely.
+template <bool E4M3, int D, int NT, int W, int S>
+__global__ void __launch_bounds__(32 * W, 1) k_paged_mma(const PagedArgs a) {
+    using Sm = MmaSmem<E4M3, D, NT, W, S>;
+    using G = typename Sm::G;
+    constexpr int KS = D / 16, MT = D / 16, ROWS = 8 * NT, THREADS = 32 * W;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Sm &sm = *reinterpret_cast<Sm *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(&sm.full[warp][s], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    paged_schedule<THREADS, W>(a, sm.sched);
+
+    const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * kPageGroups * G::kGroup;
+    uint32_t skip = 0;      // stages whose group's page id is bad: nothing was copied
+    uint32_t pending = 0;   // stages with a copy that has not been waited for
+    bool dead = false;      // a wait gave up: no further copies, no further waits
+    Feeder<W> feed;
+    feed.begin(a, sm.sched, warp);
+    const auto issue = [&](int s) {
+        if (!feed.live || dead) return;
+        if (feed.page < 0 || feed.page >= a.num_pages) {
+            if (lane == 0) {
+                raise_flag(a.flags, FLAG_BAD_PAGE);
+                mbar_arrive(&sm.full[warp][s]);
+            }
+            skip |= 1u << s;
+        } else {
+            skip &= ~(1u << s);
+            if (lane == 0) {
+                const uint8_t *src = a.pages + feed.page * page_bytes +
+                                     (static_cast<int64_t>(feed.p.h) * kPageGroups + feed.g % kPageGroups) * G::kGroup;
+                mbar_arrive_expect_tx(&sm.full[warp][s], G::kGroup);
+                bulk_g2s(sm.ring[warp][s], src, G::kGroup, &sm.full[warp][s]);
+            }
+        }
+        pending |= 1u << s;
+        feed.step(a, sm.sched, warp);
+    };
+#pragma unroll 1
+    for (int s = 0; s < S; ++s) issue(s);
+
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
+    const float cap_l2 = a.softcap * kLog2e;
+    int stage = 0;
+    uint32_t phase = 0;
+    PagedWalk walk;
+    PagedPiece pc;
+    walk.begin(a, sm.sched);
+    while (walk.next(a, sm.sched, &pc)) {
+        const int row0 = pc.pass * ROWS, rows = min(ROWS, a.rows - row0);
+        // the pass's query rows, one warp per row: e4m3 caches take them as fp16, scaled by a power of two
+        // that puts the largest finite element into [2^14, 2^15): exact down to 2^-29 of it
+        for (int r = warp; r < ROWS; r += W) {
+            constexpr int PER = D / 32;
+            float x[PER] = {};
+            float fac = a.scale, slope = 0.f;
+            if (r < rows) {
+                const int rr = (row0 + r) / a.G, hq = pc.h * a.G + (row0 + r) % a.G;
+                const __nv_bfloat16 *src = q + pc.b * a.q_b + rr * a.q_r + hq * a.q_h + lane * PER;
+                if constexpr (PER == 4) {
+                    const float4 v = load4(src);
+                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                } else {
+                    const uint32_t u = *reinterpret_cast<const uint32_t *>(src);
+                    x[0] = bf16lo(u), x[1] = bf16hi(u);
+                }
+                if (a.slopes) slope = a.slopes[hq];
+            }
+            if constexpr (E4M3) {
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) top = fabsf(x[i]) < INFINITY ? fmaxf(top, fabsf(x[i])) : top;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // 2^(14 - exponent), kept within fp32's normal powers
+                const int up = min(max(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), -113), 126);
+                const float mul = top > 0.f ? scale_of(127 + up) : 1.f;
+                fac = top > 0.f ? fac * scale_of(127 - up) : fac;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) x[i] *= mul;
+            }
+            uint32_t *dst = reinterpret_cast<uint32_t *>(sm.q[r] + lane * PER * 2);
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) dst[i / 2] = E4M3 ? pack_f16x2(x[i], x[i + 1]) : pack_bf16x2(x[i], x[i + 1]);
+            if (lane == 0) {
+                sm.qfac[r] = a.softcap > 0.f ? fac / a.softcap : fac * kLog2e;
+                sm.slope[r] = slope * kLog2e;
+            }
+        }
+        __syncthreads();
+        const int lo = sm.sched.lo[pc.b], hi = sm.sched.hi[pc.b], g0 = lo / kGroupTokens;
+        const int g_end = hi > lo ? min((hi + kGroupTokens - 1) / kGroupTokens, g0 + pc.r1 * W) : 0;
+        // element pairs d0, d0 + 1 and d0 + 2, d0 + 3 of row g of tile nt for step ks
+        const auto qfrag = [&](int nt, int ks) {
+            const int d0 = E4M3 ? 64 * (ks / 4) + 16 * tq + 4 * (ks % 4) : 32 * (ks / 2) + 8 * tq + 4 * (ks % 2);
+            return *reinterpret_cast<const uint2 *>(sm.q[8 * nt + g] + 2 * d0);
+        };
+        uint2 qf[NT == 1 ? KS : 1];
+        if constexpr (NT == 1) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) qf[ks] = qfrag(0, ks);
+        }
+        float fac[NT][2], slope[NT][2], mref[NT][2], l[NT][2], o[NT][MT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                fac[nt][c] = sm.qfac[8 * nt + 2 * tq + c];
+                slope[nt][c] = sm.slope[8 * nt + 2 * tq + c];
+                mref[nt][c] = -3.402823466e38f;   // finite: a masked logit (-inf) less it is -inf, not NaN
+                l[nt][c] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[nt][j][c] = 0.f;
+        }
+#pragma unroll 1
+        for (int gi = g0 + pc.r0 * W + warp; gi < g_end; gi += W) {
+            if (!dead && !mbar_wait(&sm.full[warp][stage], phase)) {
+                dead = true;
+                if (lane == 0) raise_flag(a.flags, FLAG_TIMEOUT);
+            }
+            dead = __any_sync(0xffffffffu, dead);
+            if (dead) continue;
+            {
+                pending &= ~(1u << stage);
+                if (!(skip >> stage & 1)) {
+                    const uint8_t *buf = sm.ring[warp][stage];
+                    const uint32_t base = smem_u32(buf);
+                    const int t0 = gi * kGroupTokens;
+                    // ---- logits: tokens g, g + 8 x rows 2 tq, 2 tq + 1 of every tile
+                    float s[NT][4], s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
+                    const uint32_t krow = base + g * G::kVec;
+                    constexpr int STEPS = E4M3 ? 4 : 2;   // steps that one 16-byte chunk serves
+#pragma unroll
+                    for (int i = 0; i < KS / STEPS; ++i) {
+                        const uint32_t at = krow + 16 * cache_chunk(4 * i + tq, g, G::kChunks);
+                        const uint4 ka = lds128(at), kb = lds128(at + 8 * G::kVec);
+#pragma unroll
+                        for (int w = 0; w < STEPS; ++w) {
+                            uint32_t a0, a1, a2, a3;
+                            if constexpr (E4M3) {
+                                a0 = cvt_lo(word(ka, w)), a2 = cvt_hi(word(ka, w));
+                                a1 = cvt_lo(word(kb, w)), a3 = cvt_hi(word(kb, w));
+                            } else {
+                                a0 = word(ka, 2 * w), a2 = word(ka, 2 * w + 1);
+                                a1 = word(kb, 2 * w), a3 = word(kb, 2 * w + 1);
+                            }
+                            const int ks = STEPS * i + w;
+                            if constexpr (NT == 1) {   // two chains
+                                if (w & 1) mma_tile<E4M3>(s2, a0, a1, a2, a3, qf[ks].x, qf[ks].y);
+                                else mma_tile<E4M3>(s[0], a0, a1, a2, a3, qf[ks].x, qf[ks].y);
+                            } else {
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    const uint2 b = qfrag(nt, ks);
+                                    mma_tile<E4M3>(s[nt], a0, a1, a2, a3, b.x, b.y);
+                                }
+                            }
+                        }
+                    }
+                    if constexpr (NT == 1) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[0][c] += s2[c];
+                    }
+                    float ve[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};
+                    float ksc[2] = {1.f, 1.f};
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t kb = buf[2 * G::kBlock + g + 8 * c];
+                            const uint32_t vb = buf[2 * G::kBlock + kGroupTokens + g + 8 * c];
+                            ksc[c] = scale_of(kb);
+                            ve[c] = static_cast<float>(static_cast<int>(vb) - 127);
+                            vinv[c] = scale_of(254 - vb);
+                        }
+                    }
+                    const float gap0 = static_cast<float>(hi - 1 - t0 - g);
+                    const bool partial = t0 < lo || t0 + kGroupTokens > hi;
+                    const bool in0 = t0 + g >= lo && t0 + g < hi, in1 = t0 + g + 8 >= lo && t0 + g + 8 < hi;
+                    bool raise = false;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            float x = s[nt][c] * fac[nt][c & 1];
+                            if constexpr (E4M3) x *= ksc[c >> 1];
+                            if (a.softcap > 0.f) x = capped(x, cap_l2);
+                            x = fmaf(-slope[nt][c & 1], gap0 - 8.f * (c >> 1), x);
+                            if constexpr (E4M3) x += ve[c >> 1];
+                            s[nt][c] = x;
+                        }
+                    if (partial) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (!in0) s[nt][0] = s[nt][1] = -INFINITY;
+                            if (!in1) s[nt][2] = s[nt][3] = -INFINITY;
+                        }
+                        if (!in0) vinv[0] = 0.f;   // an exponent byte behind the end may be anything
+                        if (!in1) vinv[1] = 0.f;
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) raise |= s[nt][c] > mref[nt][c & 1] + 8.f;
+                    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float top = fmaxf(s[nt][c], s[nt][c + 2]);
+#pragma unroll
+                                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                                top = fmaxf(top, mref[nt][c]);
+                                const float f = ex2(mref[nt][c] - top);
+                                mref[nt][c] = top;
+                                l[nt][c] *= f;
+#pragma unroll
+                                for (int j = 0; j < MT; ++j) o[nt][j][c] *= f, o[nt][j][c + 2] *= f;
+                            }
+                    }
+                    uint32_t pb[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float p[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            p[c] = ex2(s[nt][c] - mref[nt][c & 1]);
+                            if constexpr (E4M3) l[nt][c & 1] = fmaf(p[c], vinv[c >> 1], l[nt][c & 1]);
+                            else l[nt][c & 1] += p[c];
+                        }
+                        pb[nt][0] = movmatrix_t(E4M3 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
+                        pb[nt][1] = movmatrix_t(E4M3 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
+                    }
+                    // ---- outputs: tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 x this lane's d
+                    const uint32_t vrow = base + G::kBlock + 2 * tq * G::kVec;
+                    constexpr int HALVES = D * G::kElem / 128 > 0 ? D * G::kElem / 128 : 1;   // 16-byte chunks per lane and row
+                    constexpr int WORDS = D * G::kElem / 32 / HALVES;                          // words of one: 4, or 2 (e4m3, d = 64)
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; ++hf) {
+                        uint32_t v[4][WORDS];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int n = 2 * tq + (r & 1) + 8 * (r >> 1);
+                            const int dn = (r & 1) + 8 * (r >> 1);
+                            if constexpr (WORDS == 4) {
+                                const uint4 u = lds128(vrow + dn * G::kVec + 16 * cache_chunk(g + 8 * hf, n, G::kChunks));
+                                v[r][0] = u.x, v[r][1] = u.y, v[r][2] = u.z, v[r][3] = u.w;
+                            } else {
+                                const uint2 u = *reinterpret_cast<const uint2 *>(
+                                    buf + G::kBlock + n * G::kVec + 16 * cache_chunk(g / 2, n, G::kChunks) + 8 * (g & 1));
+                                v[r][0] = u.x, v[r][1] = u.y;
+                            }
+                            if (partial && (t0 + n < lo || t0 + n >= hi)) {   // weight 0 times what is there may be NaN
+#pragma unroll
+                                for (int w = 0; w < WORDS; ++w) v[r][w] = 0;
+                            }
+                        }
+#pragma unroll
+                        for (int w = 0; w < WORDS; ++w) {
+                            if constexpr (E4M3) {
+                                const uint32_t lo01 = __byte_perm(v[0][w], v[1][w], 0x5140);
+                                const uint32_t lo23 = __byte_perm(v[2][w], v[3][w], 0x5140);
+                                const uint32_t hi01 = __byte_perm(v[0][w], v[1][w], 0x7362);
+                                const uint32_t hi23 = __byte_perm(v[2][w], v[3][w], 0x7362);
+                                const uint32_t a0 = cvt_lo(lo01), a1 = cvt_hi(lo01), a2 = cvt_lo(lo23), a3 = cvt_hi(lo23);
+                                const uint32_t b0 = cvt_lo(hi01), b1 = cvt_hi(hi01), b2 = cvt_lo(hi23), b3 = cvt_hi(hi23);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma_f16(o[nt][2 * w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                                    mma_f16(o[nt][2 * w + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+                                }
+                            } else {
+                                const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
+                                const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+                                const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
+                                const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma_bf16(o[nt][WORDS * hf + w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();   // every lane has read the stage
+                issue(stage);
+            }
+            if (++stage == S) stage = 0, phase ^= 1;
+        }
+        // ---- join the warps, one tile of 8 rows at a time
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float sum = l[nt][c];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                if (g == 0) {
+                    sm.m[warp][8 * nt + 2 * tq + c] = mref[nt][c];
+                    sm.l[warp][8 * nt + 2 * tq + c] = sum;
+                }
+            }
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) +
+                             (walk.start_of(blockIdx.x) == pc.unit0 + pc.r0 ? 0 : 1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sm.o[warp][c * MT + j][lane] = o[nt][j][c];
+            __syncthreads();
+            for (int i = tid; i < 8 * (D / 4); i += THREADS) {
+                const int r8 = i / (D / 4), r = 8 * nt + r8, d0 = (i % (D / 4)) * 4;
+                if (r >= rows) continue;
+                float top = sm.m[0][r];
+#pragma unroll
+                for (int w = 1; w < W; ++w) top = fmaxf(top, sm.m[w][r]);
+                // where d0 .. d0 + 3 lie: lane group g, tiles j and j + 1, elements c and c + 2
+                int gd, j;
+                if constexpr (!E4M3 && D == 128) gd = d0 % 64 / 8, j = 4 * (d0 / 64) + d0 % 8 / 2;
+                else gd = d0 / (D / 8), j = d0 % (D / 8) / 2;
+                const int ln = 4 * gd + r8 / 2, c = r8 & 1;
+                float sum = 0.f;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float f = ex2(sm.m[w][r] - top);
+                    sum = fmaf(f, sm.l[w][r], sum);
+                    x.x = fmaf(f, sm.o[w][c * MT + j][ln], x.x);
+                    x.y = fmaf(f, sm.o[w][(c + 2) * MT + j][ln], x.y);
+                    x.z = fmaf(f, sm.o[w][c * MT + j + 1][ln], x.z);
+                    x.w = fmaf(f, sm.o[w][(c + 2) * MT + j + 1][ln], x.w);
+                }
+                const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+                x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+                const float l2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+                if (pc.whole) {
+                    paged_write<__nv_bfloat16, D>(a, pc.b, pc.h, row0 + r, d0, x, l2);
+                } else {
+                    store4(a.part_o + (slot * ROWS + r) * D + d0, x);
+                    if (d0 == 0) a.part_l[slot * ROWS + r] = l2;
+                }
+            }
+            __syncthreads();
+        }
+        if (!pc.whole) paged_finish_piece<__nv_bfloat16, D, ROWS, THREADS>(a, walk, pc, sm.sched);
+    }
+    // a warp that gave up leaves only when the copies that it issued have landed (bounded again)
+    if (dead)
+        for (int s = 0; s < S; ++s)
+            if (pending >> s & 1) mbar_wait(&sm.full[warp][s], s < stage ? phase ^ 1 : phase);
+}
+
 // CTAs of a kernel that fit the current device at once (kept per kernel and device in a fixed table:
 // nothing here allocates or throws).
 struct GridEntry {
@@ -280,15 +742,30 @@ cudaError_t launch_simple(const PagedArgs &a, cudaStream_t s) {
     return launch(k_paged_f32<T, E4M3, 64>, a, kSimpleThreads, sizeof(SimpleSmem<64>), s);
 }
 
+template <bool E4M3, int D, int NT, int W, int S>
+cudaError_t launch_mma(const PagedArgs &a, cudaStream_t s) {
+    return launch(k_paged_mma<E4M3, D, NT, W, S>, a, 32 * W, sizeof(MmaSmem<E4M3, D, NT, W, S>) + 128, s);
+}
+
+template <bool E4M3, int D, int W, int S>
+cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
+    if (a.pass_rows == 8) return launch_mma<E4M3, D, 1, W, S>(a, s);
+    if (a.pass_rows == 16) return launch_mma<E4M3, D, 2, W, S>(a, s);
+    return launch_mma<E4M3, D, 4, W, S>(a, s);
+}
+
 }  // namespace
 
-int paged_pass_rows(int dtype, int rows) { return kSimplePass; }
+int paged_pass_rows(int dtype, int rows) {
+    if (dtype == SKV_F32) return kSimplePass;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
 
 cudaError_t launch_paged_attn(const PagedArgs &a, cudaStream_t s) {
     if (a.dtype == SKV_F32)
         return a.format == SKV_CACHE_E4M3 ? launch_simple<float, true>(a, s) : launch_simple<float, false>(a, s);
-    return a.format == SKV_CACHE_E4M3 ? launch_simple<__nv_bfloat16, true>(a, s)
-                                      : launch_simple<__nv_bfloat16, false>(a, s);
+    if (a.format == SKV_CACHE_E4M3) return a.d == 128 ? launch_rows<true, 128, 8, 5>(a, s) : launch_rows<true, 64, 8, 8>(a, s);
+    return a.d == 128 ? launch_rows<false, 128, 8, 2>(a, s) : launch_rows<false, 64, 8, 4>(a, s);
 }
 
 }  // namespace skv

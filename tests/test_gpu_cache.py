@@ -376,7 +376,10 @@ def test_strided_queries_other_stream_and_shared_workspace():
     cache, table, g = filled(B, Hkv, d, BF, "e4m3", lens, seed=6)
     x = torch.randn(B, R, Hq + 2 * Hkv, d, generator=g).bfloat16().cuda()
     q = x[:, :, :Hq]
-    ws = torch.zeros(skv.paged_attn_workspace_bytes(64, R, Hq, Hkv, d, 64), dtype=torch.uint8, device="cuda")
+    others = ((64, 1, 1, 64, 40), (1, 8, 4, 128, 3000))
+    size = max([skv.paged_attn_workspace_bytes(B, R, Hq, Hkv, d, table.shape[1])] +
+               [skv.paged_attn_workspace_bytes(B2, R2, H2, 1, d2, skv.token_pages_for(n)) for B2, R2, H2, d2, n in others])
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
     want = skv.paged_attn(q.contiguous(), cache, table, i32(lens), workspace=ws)
     got = skv.paged_attn(q, cache, table, i32(lens), workspace=ws)
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
@@ -386,7 +389,7 @@ def test_strided_queries_other_stream_and_shared_workspace():
     s.synchronize()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     # other shapes through the same workspace, and the first again
-    for B2, R2, H2, d2, n in ((64, 1, 1, 64, 40), (1, 8, 4, 128, 3000)):
+    for B2, R2, H2, d2, n in others:
         c2, t2, _ = filled(B2, 1, d2, BF, "raw", [n] * B2, seed=n)
         q2 = torch.randn(B2, R2, H2, d2, generator=g).bfloat16().cuda()
         a = skv.paged_attn(q2, c2, t2, i32([n] * B2), workspace=ws)
