@@ -53,6 +53,7 @@ skv_status plan_paged(int dtype, int B, int R, int Hq, int Hkv, int d, int max_p
     a->Hq = Hq;
     a->Hkv = Hkv;
     a->G = Hq / Hkv;
+    a->inv_G = 1.0f / static_cast<float>(a->G);
     a->d = d;
     a->dtype = dtype;
     a->rows = static_cast<int>(rows);
@@ -60,8 +61,8 @@ skv_status plan_paged(int dtype, int B, int R, int Hq, int Hkv, int d, int max_p
     a->passes = (a->rows + a->pass_rows - 1) / a->pass_rows;
     const int64_t per_seq = static_cast<int64_t>(Hkv) * a->passes;
     if (per_seq * B > kMaxPagedUnits) return SKV_ERR_UNSUPPORTED;
-    // the rounds (of at least 8 groups) of one sequence's units are counted in int32
-    if (per_seq * (static_cast<int64_t>(max_pages) * kPageGroups / 8 + 2) > INT32_MAX) return SKV_ERR_UNSUPPORTED;
+    // the weight (rounds of at least 4 groups, and a cost) of one sequence's units is counted in int32
+    if (per_seq * (static_cast<int64_t>(max_pages) * kPageGroups / 4 + 16) > INT32_MAX) return SKV_ERR_UNSUPPORTED;
     *total = kPartOffset + align256(static_cast<size_t>(kMaxPagedCtas) * 2 * a->pass_rows * d * 4) +
              align256(static_cast<size_t>(kMaxPagedCtas) * 2 * a->pass_rows * 4);
     return SKV_OK;

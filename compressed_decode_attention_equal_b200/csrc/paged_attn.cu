@@ -16,15 +16,22 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// cap tanh(x / cap) with t = x / cap given: tanh t = 1 - 2 / (e^(2t) + 1), whose absolute error is a few
-// 2^-24 over the whole range (the hardware tanh's 2^-11 would show in the logits)
+// cap tanh(t) with tanh t = 1 - 2 / (e^(2t) + 1), whose absolute error stays within a few ulps of 1 over the
+// whole range (the hardware tanh's 2^-11 would show in the logits): with a true division for fp32 results,
+// with the approximate exponential and reciprocal (2^-22 and 2^-23 relative) in front of 16-bit products.
+__device__ __forceinline__ float capped_exact(float t, float cap) {
+    return cap * (1.0f - 2.0f / (exp2f(t * (2.0f * kLog2e)) + 1.0f));
+}
 __device__ __forceinline__ float capped(float t, float cap) {
-    const float e = exp2f(t * (2.0f * kLog2e));
-    return cap * (1.0f - 2.0f / (e + 1.0f));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(t * (2.0f * kLog2e)) + 1.0f));
+    return fmaf(-2.0f * cap, r, cap);
 }
 
 constexpr int kSimpleWarps = 8, kSimpleThreads = 32 * kSimpleWarps, kSimplePass = 8;
 constexpr int kSimpleRound = 2 * kSimpleWarps;   // token groups of a round: 32 tokens per warp
+constexpr int kSimpleCost = 1;
+constexpr int kSimpleMaxCtas = 480;              // the join keeps a word per row and piece where the outputs are
 
 template <int D>
 struct SimpleSmem {
@@ -45,16 +52,24 @@ __global__ void __launch_bounds__(kSimpleThreads) k_paged_f32(const PagedArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    paged_schedule<kSimpleThreads, kSimpleRound>(a, sm.sched);
-    PagedWalk walk;
-    walk.begin(a, sm.sched);
-    PagedPiece pc;
+    paged_schedule<kSimpleThreads, kSimpleRound, kSimpleCost>(a, sm.sched);
+    paged_pieces<kSimpleRound, kSimpleCost, 1>(a, sm.sched, 0);
     const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * kPageGroups * G::kGroup;
     const T *q = static_cast<const T *>(a.q);
-    while (walk.next(a, sm.sched, &pc)) {
+    for (int from = 0, i = 0;; ++i) {
+        i = paged_next(sm.sched, i);
+        if (i == sm.sched.n) {
+            if (i < kPieceTable) break;
+            __syncthreads();
+            from += kPieceTable;
+            paged_pieces<kSimpleRound, kSimpleCost, 1>(a, sm.sched, from);
+            i = -1;
+            continue;
+        }
+        const PagedPiece pc = sm.sched.piece[i];
         const int row0 = pc.pass * NR, rows = min(NR, a.rows - row0);
-        for (int i = tid; i < NR * D; i += kSimpleThreads) {
-            const int r = i / D, d = i % D;
+        for (int e = tid; e < NR * D; e += kSimpleThreads) {
+            const int r = e / D, d = e % D;
             float x = 0.f;
             if (r < rows) {
                 const int rr = (row0 + r) / a.G, g = (row0 + r) % a.G;
@@ -67,8 +82,7 @@ __global__ void __launch_bounds__(kSimpleThreads) k_paged_f32(const PagedArgs a)
         for (int r = 0; r < NR; ++r)
             slope[r] = a.slopes && r < rows ? a.slopes[pc.h * a.G + (row0 + r) % a.G] : 0.f;
         __syncthreads();
-        const int lo = sm.sched.lo[pc.b], hi = sm.sched.hi[pc.b];
-        const int g0 = lo / kGroupTokens;
+        const int lo = pc.lo, hi = pc.hi, g0 = lo / kGroupTokens;
         const int t_end = min(hi, (g0 + pc.r1 * kSimpleRound) * kGroupTokens);
         float m[NR], l[NR], o[NR][PER];
 #pragma unroll
@@ -100,10 +114,18 @@ __global__ void __launch_bounds__(kSimpleThreads) k_paged_f32(const PagedArgs a)
             float vs = 1.f;
             if (valid) {
                 const uint8_t *key = grp + n * G::kVec;
-#pragma unroll 2
-                for (int c = 0; c < G::kChunks; ++c) {
+                constexpr int AHEAD = G::kChunks < 8 ? G::kChunks : 8;   // loads in flight per lane
+#pragma unroll 1
+                for (int c0 = 0; c0 < G::kChunks; c0 += AHEAD) {
+                  uint4 raw[AHEAD];
+#pragma unroll
+                  for (int e = 0; e < AHEAD; ++e)
+                      raw[e] = *reinterpret_cast<const uint4 *>(key + 16 * cache_chunk(c0 + e, n, G::kChunks));
+#pragma unroll
+                  for (int e = 0; e < AHEAD; ++e) {
+                    const int c = c0 + e;
                     float x[CV::N];
-                    CV::get(*reinterpret_cast<const uint4 *>(key + 16 * cache_chunk(c, n, G::kChunks)), x);
+                    CV::get(raw[e], x);
 #pragma unroll
                     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -114,6 +136,7 @@ __global__ void __launch_bounds__(kSimpleThreads) k_paged_f32(const PagedArgs a)
                             s[r] = fmaf(x[i + 2], y.z, s[r]);
                             s[r] = fmaf(x[i + 3], y.w, s[r]);
                         }
+                  }
                 }
                 float ks = a.scale;
                 if constexpr (E4M3) {
@@ -124,7 +147,7 @@ __global__ void __launch_bounds__(kSimpleThreads) k_paged_f32(const PagedArgs a)
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
                     s[r] *= ks;
-                    if (a.softcap > 0.f) s[r] = capped(s[r] / a.softcap, a.softcap);
+                    if (a.softcap > 0.f) s[r] = capped_exact(s[r] / a.softcap, a.softcap);
                     s[r] = (s[r] - slope[r] * gap) * kLog2e;
                 }
             } else {
@@ -150,7 +173,7 @@ __global__ void __launch_bounds__(kSimpleThreads) k_paged_f32(const PagedArgs a)
             // values: lane = dimensions
             const uint32_t mask = __ballot_sync(0xffffffffu, valid);
             const uint64_t base = reinterpret_cast<uint64_t>(grp);
-#pragma unroll 4
+#pragma unroll 16
             for (int j = 0; j < 32; ++j) {
                 if (!(mask >> j & 1)) continue;   // masked rows are not read: they may hold anything
                 const uint8_t *g = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, base, j));
@@ -210,37 +233,44 @@ __global__ void __launch_bounds__(kSimpleThreads) k_paged_f32(const PagedArgs a)
             const float inv = sum == 0.f ? 0.f : 1.0f / sum;
             x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
             const float l2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-            if (pc.whole) {
+            if (pc.np == 1) {
                 paged_write<T, D>(a, pc.b, pc.h, row0 + r, d0, x, l2);
             } else {
-                const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) +
-                                      (walk.start_of(blockIdx.x) == pc.unit0 + pc.r0 ? 0 : 1)) * NR + r;
+                const int64_t slot = pc.slot(blockIdx.x) * NR + r;
                 store4(a.part_o + slot * D + d0, x);
                 if (d0 == 0) a.part_l[slot] = l2;
             }
         }
-        if (pc.whole) __syncthreads();
-        else paged_finish_piece<T, D, NR, kSimpleThreads>(a, walk, pc, sm.sched);
+        if (pc.np == 1) __syncthreads();
+        else paged_finish_piece<T, D, NR, kSimpleThreads>(a, pc, sm.sched, &sm.o[0][0][0]);
     }
 }
 
 // ---------------------------------------------------------------------------
 // bf16 queries: tensor cores
 // ---------------------------------------------------------------------------
-// Shared memory of k_paged_mma<E4M3, D, NT, W, S>: per warp a ring of S token groups, each one bulk
+// Shared memory of k_paged_mma<E4M3, D, NT, W, S, CTAS>: per warp a ring of S token groups, each one bulk
 // copy; the pass's query rows; the warps' outputs at the end of a piece.
-template <bool E4M3, int D, int NT, int W, int S>
+template <bool E4M3, int D, int NT, int W, int S, int CTAS>
 struct MmaSmem {
     using G = CacheGeom<__nv_bfloat16, E4M3, D>;
     static constexpr int kStage = (G::kGroup + 127) / 128 * 128;
     static constexpr int kRows = 8 * NT;
+    // rounds that a unit's query load and outputs take as long as: 1, 2, 3, 4 measured 90.0, 74.9, 76.8, 80.0 us
+    // (64 ragged sequences x 16 heads, one row each), and 2, 3, 4 with 28 rows 48.4, 49.5, 47.1 us (48 x 4 heads)
+    static constexpr int kCost = NT == 1 ? 2 : 4;
+    // least weight per CTA: one sequence of 10,500 tokens and 2 heads 14.3 us at 2, 15.5 us at 4
+    static constexpr int kLeast = 2;
     static constexpr int kQRow = 2 * D + 8;      // bytes of a query row: 8 more than 2 D against bank conflicts
     static constexpr int kMerge = 33;            // words per accumulator element of a warp's 32 lanes
+    static constexpr int kMaxCtas = CTAS * 160;  // the join of a unit's pieces keeps a word per row and piece in o
+    static constexpr int kOut = W * 4 * (D / 16) * kMerge;
+    static constexpr int kJoin = kRows * (kMaxCtas + 1);
     alignas(128) uint8_t ring[W][S][kStage];
-    float o[W][4 * (D / 16)][kMerge];            // one tile of 8 rows of all warps
+    float o[kOut > kJoin ? kOut : kJoin];        // one tile of 8 rows of all warps: [W][4 D / 16][kMerge]
     alignas(16) uint8_t q[kRows][kQRow];
     float qfac[kRows], slope[kRows];
-    float m[W][kRows], l[W][kRows];
+    float m[W][kRows], l[W][kRows], part[kRows];
     alignas(8) uint64_t full[W][S];
     PagedSched sched;
 };
@@ -270,37 +300,39 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
-// The token groups that one warp of a CTA takes, in order, over all pieces of the CTA's range: what
-// runs ahead of the computation to issue the copies. The page id of the group that comes next is
-// loaded one step before it is needed.
+// The token groups that one warp of a CTA takes, in order, over the pieces of the table: what runs
+// ahead of the computation to issue the copies. The lanes hold the page ids of the next 32 groups of a
+// piece, loaded together.
 template <int W>
 struct Feeder {
-    PagedWalk walk;
-    PagedPiece p;
-    int g, g_end, page;
-    bool live;
+    int i;                 // piece of the table; the table's n: no more groups
+    int g, g_end, ids, at; // this group, the piece's end, lane j: page id of the j-th group after the load, groups since
 
-    __device__ __forceinline__ void settle(const PagedArgs &a, const PagedSched &s, int warp) {
-        while (g >= g_end) {
-            if (!walk.next(a, s, &p)) {
-                live = false;
-                return;
-            }
-            const int lo = s.lo[p.b], hi = s.hi[p.b], g0 = lo / kGroupTokens;
-            g = g0 + p.r0 * W + warp;
-            g_end = hi > lo ? min((hi + kGroupTokens - 1) / kGroupTokens, g0 + p.r1 * W) : 0;
-        }
-        page = ld_global_s32(a.page_table + static_cast<int64_t>(p.b) * a.max_pages + g / kPageGroups);
+    __device__ __forceinline__ void load_ids(const PagedArgs &a, const PagedSched &s) {
+        const int mine = g + W * static_cast<int>(threadIdx.x & 31);
+        ids = mine < g_end ? ld_global_s32(a.page_table + static_cast<int64_t>(s.piece[i].b) * a.max_pages + mine / kPageGroups)
+                           : -1;
+        at = 0;
     }
-    __device__ __forceinline__ void begin(const PagedArgs &a, const PagedSched &s, int warp) {
-        walk.begin(a, s);
-        g = g_end = 0;
-        live = true;
-        settle(a, s, warp);
+    __device__ __forceinline__ int page() const { return __shfl_sync(0xffffffffu, ids, at); }
+    // to the first group of piece i or, where this warp has none there, of the pieces after it
+    __device__ __forceinline__ void settle(const PagedArgs &a, const PagedSched &s, int warp) {
+        for (; i < s.n; ++i) {
+            const PagedPiece &p = s.piece[i];
+            const int g0 = p.lo / kGroupTokens;
+            g = g0 + p.r0 * W + warp;
+            g_end = p.hi > p.lo ? min((p.hi + kGroupTokens - 1) / kGroupTokens, g0 + p.r1 * W) : 0;
+            if (g < g_end) break;
+        }
+        if (i < s.n) load_ids(a, s);
     }
     __device__ __forceinline__ void step(const PagedArgs &a, const PagedSched &s, int warp) {
         g += W;
-        settle(a, s, warp);
+        if (++at == 32 && g < g_end) load_ids(a, s);
+        if (g >= g_end) {
+            ++i;
+            settle(a, s, warp);
+        }
     }
 };
 
@@ -323,9 +355,9 @@ struct Feeder {
 //   Weights are rounded to the matrix type (fp16 2^-11, bf16 2^-8 relative): the second product runs on
 //   16-bit operands, and the partition keeps the fp32 weights. Sums and maxima are fp32. The reference maximum
 //   moves only when a logit exceeds it by 2^8, so that the rescale of O runs rarely.
-template <bool E4M3, int D, int NT, int W, int S>
-__global__ void __launch_bounds__(32 * W, 1) k_paged_mma(const PagedArgs a) {
-    using Sm = MmaSmem<E4M3, D, NT, W, S>;
+template <bool E4M3, int D, int NT, int W, int S, int CTAS>
+__global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
+    using Sm = MmaSmem<E4M3, D, NT, W, S, CTAS>;
     using G = typename Sm::G;
     constexpr int KS = D / 16, MT = D / 16, ROWS = 8 * NT, THREADS = 32 * W;
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -338,17 +370,18 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_mma(const PagedArgs a) {
     __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    paged_schedule<THREADS, W>(a, sm.sched);
+    paged_schedule<THREADS, W, Sm::kCost>(a, sm.sched);
+    paged_pieces<W, Sm::kCost, Sm::kLeast>(a, sm.sched, 0);
 
     const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * kPageGroups * G::kGroup;
     uint32_t skip = 0;      // stages whose group's page id is bad: nothing was copied
     uint32_t pending = 0;   // stages with a copy that has not been waited for
     bool dead = false;      // a wait gave up: no further copies, no further waits
-    Feeder<W> feed;
-    feed.begin(a, sm.sched, warp);
+    Feeder<W> feed{};
     const auto issue = [&](int s) {
-        if (!feed.live || dead) return;
-        if (feed.page < 0 || feed.page >= a.num_pages) {
+        if (feed.i >= sm.sched.n || dead) return;
+        const int page = feed.page();
+        if (page < 0 || page >= a.num_pages) {
             if (lane == 0) {
                 raise_flag(a.flags, FLAG_BAD_PAGE);
                 mbar_arrive(&sm.full[warp][s]);
@@ -357,8 +390,8 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_mma(const PagedArgs a) {
         } else {
             skip &= ~(1u << s);
             if (lane == 0) {
-                const uint8_t *src = a.pages + feed.page * page_bytes +
-                                     (static_cast<int64_t>(feed.p.h) * kPageGroups + feed.g % kPageGroups) * G::kGroup;
+                const uint8_t *src = a.pages + page * page_bytes +
+                                     (static_cast<int64_t>(sm.sched.piece[feed.i].h) * kPageGroups + feed.g % kPageGroups) * G::kGroup;
                 mbar_arrive_expect_tx(&sm.full[warp][s], G::kGroup);
                 bulk_g2s(sm.ring[warp][s], src, G::kGroup, &sm.full[warp][s]);
             }
@@ -366,59 +399,88 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_mma(const PagedArgs a) {
         pending |= 1u << s;
         feed.step(a, sm.sched, warp);
     };
-#pragma unroll 1
-    for (int s = 0; s < S; ++s) issue(s);
-
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
+    constexpr int PER = D / 32, RPW = (ROWS + W - 1) / W;   // query elements per lane and row, rows per warp
+    uint32_t qx[RPW][PER / 2];
+    float qslope[RPW];
+    const auto load_queries = [&](const PagedPiece &p) {
+        const int row0 = p.pass * ROWS, rows = min(ROWS, a.rows - row0);
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + p.b * a.q_b + static_cast<int64_t>(p.h) * a.G * a.q_h + lane * PER;
+#pragma unroll
+        for (int i = 0; i < RPW; ++i) {
+            const int r = warp + W * i;
+            qslope[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < PER / 2; ++e) qx[i][e] = 0;
+            if (r < rows) {
+                const int rr = static_cast<int>((row0 + r + 0.5f) * a.inv_G), gq = row0 + r - rr * a.G;
+                const __nv_bfloat16 *src = q + rr * a.q_r + gq * a.q_h;
+                if constexpr (PER == 4) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                    qx[i][0] = u.x, qx[i][1] = u.y;
+                } else {
+                    qx[i][0] = *reinterpret_cast<const uint32_t *>(src);
+                }
+                if (a.slopes) qslope[i] = a.slopes[p.h * a.G + gq];
+            }
+        }
+    };
     const float cap_l2 = a.softcap * kLog2e;
     int stage = 0;
     uint32_t phase = 0;
-    PagedWalk walk;
-    PagedPiece pc;
-    walk.begin(a, sm.sched);
-    while (walk.next(a, sm.sched, &pc)) {
+    int from = 0, at = paged_next(sm.sched, 0);
+    bool fresh = true;   // a new table: nothing is ahead
+#pragma unroll 1
+    while (true) {
+        if (at == sm.sched.n) {
+            if (at < kPieceTable) break;
+            __syncthreads();
+            from += kPieceTable;
+            paged_pieces<W, Sm::kCost, Sm::kLeast>(a, sm.sched, from);
+            at = paged_next(sm.sched, 0);
+            fresh = true;
+            continue;
+        }
+        const PagedPiece &pc = sm.sched.piece[at];
+        if (fresh) {   // the queries' loads before anything waits, then the ring
+            load_queries(pc);
+            feed.i = 0;
+            feed.settle(a, sm.sched, warp);
+#pragma unroll 1
+            for (int s = 0; s < S; ++s) issue(stage + s < S ? stage + s : stage + s - S);
+            fresh = false;
+        }
         const int row0 = pc.pass * ROWS, rows = min(ROWS, a.rows - row0);
         // the pass's query rows, one warp per row: e4m3 caches take them as fp16, scaled by a power of two
         // that puts the largest finite element into [2^14, 2^15): exact down to 2^-29 of it
-        for (int r = warp; r < ROWS; r += W) {
-            constexpr int PER = D / 32;
-            float x[PER] = {};
-            float fac = a.scale, slope = 0.f;
-            if (r < rows) {
-                const int rr = (row0 + r) / a.G, hq = pc.h * a.G + (row0 + r) % a.G;
-                const __nv_bfloat16 *src = q + pc.b * a.q_b + rr * a.q_r + hq * a.q_h + lane * PER;
-                if constexpr (PER == 4) {
-                    const float4 v = load4(src);
-                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-                } else {
-                    const uint32_t u = *reinterpret_cast<const uint32_t *>(src);
-                    x[0] = bf16lo(u), x[1] = bf16hi(u);
-                }
-                if (a.slopes) slope = a.slopes[hq];
-            }
+#pragma unroll
+        for (int i = 0; i < RPW; ++i) {
+            const int r = warp + W * i;
+            if (r >= ROWS) break;
+            float x[PER], fac = a.scale;
+#pragma unroll
+            for (int e = 0; e < PER; e += 2) x[e] = bf16lo(qx[i][e / 2]), x[e + 1] = bf16hi(qx[i][e / 2]);
             if constexpr (E4M3) {
                 float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) top = fabsf(x[i]) < INFINITY ? fmaxf(top, fabsf(x[i])) : top;
+                for (int e = 0; e < PER; ++e) top = fabsf(x[e]) < INFINITY ? fmaxf(top, fabsf(x[e])) : top;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                // 2^(14 - exponent), kept within fp32's normal powers
-                const int up = min(max(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), -113), 126);
+                const int up = min(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 126);   // >= -113
                 const float mul = top > 0.f ? scale_of(127 + up) : 1.f;
                 fac = top > 0.f ? fac * scale_of(127 - up) : fac;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) x[i] *= mul;
+                for (int e = 0; e < PER; ++e) x[e] *= mul;
             }
             uint32_t *dst = reinterpret_cast<uint32_t *>(sm.q[r] + lane * PER * 2);
 #pragma unroll
-            for (int i = 0; i < PER; i += 2) dst[i / 2] = E4M3 ? pack_f16x2(x[i], x[i + 1]) : pack_bf16x2(x[i], x[i + 1]);
+            for (int e = 0; e < PER; e += 2) dst[e / 2] = E4M3 ? pack_f16x2(x[e], x[e + 1]) : pack_bf16x2(x[e], x[e + 1]);
             if (lane == 0) {
                 sm.qfac[r] = a.softcap > 0.f ? fac / a.softcap : fac * kLog2e;
-                sm.slope[r] = slope * kLog2e;
+                sm.slope[r] = qslope[i] * kLog2e;
             }
         }
         __syncthreads();
-        const int lo = sm.sched.lo[pc.b], hi = sm.sched.hi[pc.b], g0 = lo / kGroupTokens;
+        const int lo = pc.lo, hi = pc.hi, g0 = lo / kGroupTokens;
         const int g_end = hi > lo ? min((hi + kGroupTokens - 1) / kGroupTokens, g0 + pc.r1 * W) : 0;
         // element pairs d0, d0 + 1 and d0 + 2, d0 + 3 of row g of tile nt for step ks
         const auto qfrag = [&](int nt, int ks) {
@@ -622,7 +684,10 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_mma(const PagedArgs a) {
             }
             if (++stage == S) stage = 0, phase ^= 1;
         }
-        // ---- join the warps, one tile of 8 rows at a time
+        const int after = paged_next(sm.sched, at + 1);
+        if (after < sm.sched.n) load_queries(sm.sched.piece[after]);   // they arrive while the warps join
+        // ---- join the warps, one tile of 8 rows at a time; those that had no group have nothing to add
+        const int act = max(1, min(W, g_end - (g0 + pc.r0 * W)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -635,50 +700,65 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_mma(const PagedArgs a) {
                     sm.l[warp][8 * nt + 2 * tq + c] = sum;
                 }
             }
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) +
-                             (walk.start_of(blockIdx.x) == pc.unit0 + pc.r0 ? 0 : 1);
+        __syncthreads();
+        static_assert(ROWS * W <= THREADS && (W & (W - 1)) == 0, "one lane per row and warp");
+        if (tid < ROWS * W) {   // the warps' weights, 2^(m - largest m) over the joint sum, and the row's partition
+            const int r = tid / W, w = tid % W;
+            const float mine = sm.m[w][r];
+            float top = mine;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+            for (int x = 1; x < W; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float f = ex2(mine - top);
+            float sum = f * sm.l[w][r];
 #pragma unroll
-            for (int j = 0; j < MT; ++j)
+            for (int x = 1; x < W; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            sm.m[w][r] = sum == 0.f ? 0.f : f * __frcp_rn(sum);
+            if (w == 0) sm.part[r] = sum == 0.f ? -INFINITY : top + __log2f(sum);
+        }
+        // one copy of this code for all tiles: each turn writes tile 0 and moves the others down
+#pragma unroll 1
+        for (int nt = 0; 8 * nt < rows; ++nt) {
+            if (warp < act) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) sm.o[warp][c * MT + j][lane] = o[nt][j][c];
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        sm.o[((warp * 4 + c) * MT + j) * Sm::kMerge + lane] = o[0][j][c];
+#pragma unroll
+                        for (int n = 0; n + 1 < NT; ++n) o[n][j][c] = o[n + 1][j][c];
+                    }
+            }
             __syncthreads();
+#pragma unroll 1
             for (int i = tid; i < 8 * (D / 4); i += THREADS) {
                 const int r8 = i / (D / 4), r = 8 * nt + r8, d0 = (i % (D / 4)) * 4;
                 if (r >= rows) continue;
-                float top = sm.m[0][r];
-#pragma unroll
-                for (int w = 1; w < W; ++w) top = fmaxf(top, sm.m[w][r]);
                 // where d0 .. d0 + 3 lie: lane group g, tiles j and j + 1, elements c and c + 2
                 int gd, j;
                 if constexpr (!E4M3 && D == 128) gd = d0 % 64 / 8, j = 4 * (d0 / 64) + d0 % 8 / 2;
                 else gd = d0 / (D / 8), j = d0 % (D / 8) / 2;
-                const int ln = 4 * gd + r8 / 2, c = r8 & 1;
-                float sum = 0.f;
+                const float *src = sm.o + ((r8 & 1) * MT + j) * Sm::kMerge + 4 * gd + r8 / 2;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const float f = ex2(sm.m[w][r] - top);
-                    sum = fmaf(f, sm.l[w][r], sum);
-                    x.x = fmaf(f, sm.o[w][c * MT + j][ln], x.x);
-                    x.y = fmaf(f, sm.o[w][(c + 2) * MT + j][ln], x.y);
-                    x.z = fmaf(f, sm.o[w][c * MT + j + 1][ln], x.z);
-                    x.w = fmaf(f, sm.o[w][(c + 2) * MT + j + 1][ln], x.w);
+#pragma unroll 4
+                for (int w = 0; w < act; ++w, src += 4 * MT * Sm::kMerge) {
+                    const float f = sm.m[w][r];
+                    x.x = fmaf(f, src[0], x.x);
+                    x.y = fmaf(f, src[2 * MT * Sm::kMerge], x.y);
+                    x.z = fmaf(f, src[Sm::kMerge], x.z);
+                    x.w = fmaf(f, src[(2 * MT + 1) * Sm::kMerge], x.w);
                 }
-                const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-                x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-                const float l2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-                if (pc.whole) {
-                    paged_write<__nv_bfloat16, D>(a, pc.b, pc.h, row0 + r, d0, x, l2);
+                if (pc.np == 1) {
+                    paged_write<__nv_bfloat16, D>(a, pc.b, pc.h, row0 + r, d0, x, sm.part[r]);
                 } else {
-                    store4(a.part_o + (slot * ROWS + r) * D + d0, x);
-                    if (d0 == 0) a.part_l[slot * ROWS + r] = l2;
+                    const int64_t to = pc.slot(blockIdx.x) * ROWS + r;
+                    store4(a.part_o + to * D + d0, x);
+                    if (d0 == 0) a.part_l[to] = sm.part[r];
                 }
             }
             __syncthreads();
         }
-        if (!pc.whole) paged_finish_piece<__nv_bfloat16, D, ROWS, THREADS>(a, walk, pc, sm.sched);
+        if (pc.np > 1) paged_finish_piece<__nv_bfloat16, D, ROWS, THREADS>(a, pc, sm.sched, sm.o);
+        at = after;
     }
     // a warp that gave up leaves only when the copies that it issued have landed (bounded again)
     if (dead)
@@ -719,10 +799,11 @@ cudaError_t resident_ctas(const void *fn, int threads, size_t smem, int *ctas) {
 }
 
 template <typename K>
-cudaError_t launch(K kernel, const PagedArgs &a0, int threads, size_t smem, cudaStream_t s) {
+cudaError_t launch(K kernel, const PagedArgs &a0, int threads, size_t smem, int max_ctas, cudaStream_t s) {
     PagedArgs a = a0;
     cudaError_t e = resident_ctas(reinterpret_cast<const void *>(kernel), threads, smem, &a.ncta);
     if (e != cudaSuccess) return e;
+    if (a.ncta > max_ctas) a.ncta = max_ctas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.ncta);
     cfg.blockDim = dim3(threads);
@@ -738,20 +819,29 @@ cudaError_t launch(K kernel, const PagedArgs &a0, int threads, size_t smem, cuda
 
 template <typename T, bool E4M3>
 cudaError_t launch_simple(const PagedArgs &a, cudaStream_t s) {
-    if (a.d == 128) return launch(k_paged_f32<T, E4M3, 128>, a, kSimpleThreads, sizeof(SimpleSmem<128>), s);
-    return launch(k_paged_f32<T, E4M3, 64>, a, kSimpleThreads, sizeof(SimpleSmem<64>), s);
+    if (a.d == 128) return launch(k_paged_f32<T, E4M3, 128>, a, kSimpleThreads, sizeof(SimpleSmem<128>),
+                  kSimpleMaxCtas, s);
+    return launch(k_paged_f32<T, E4M3, 64>, a, kSimpleThreads, sizeof(SimpleSmem<64>),
+                  kSimpleMaxCtas, s);
 }
 
-template <bool E4M3, int D, int NT, int W, int S>
+template <bool E4M3, int D, int NT, int W, int S, int CTAS>
 cudaError_t launch_mma(const PagedArgs &a, cudaStream_t s) {
-    return launch(k_paged_mma<E4M3, D, NT, W, S>, a, 32 * W, sizeof(MmaSmem<E4M3, D, NT, W, S>) + 128, s);
+    return launch(k_paged_mma<E4M3, D, NT, W, S, CTAS>, a, 32 * W, sizeof(MmaSmem<E4M3, D, NT, W, S, CTAS>) + 128,
+                  MmaSmem<E4M3, D, NT, W, S, CTAS>::kMaxCtas, s);
 }
 
-template <bool E4M3, int D, int W, int S>
+template <bool E4M3, int D>
 cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
-    if (a.pass_rows == 8) return launch_mma<E4M3, D, 1, W, S>(a, s);
-    if (a.pass_rows == 16) return launch_mma<E4M3, D, 2, W, S>(a, s);
-    return launch_mma<E4M3, D, 4, W, S>(a, s);
+    if constexpr (E4M3) {
+        if (a.pass_rows == 8) return launch_mma<E4M3, D, 1, 8, 2, 2>(a, s);
+        if (a.pass_rows == 16) return launch_mma<E4M3, D, 2, 8, 3, 1>(a, s);
+        return launch_mma<E4M3, D, 4, 8, 3, 1>(a, s);
+    } else {
+        if (a.pass_rows == 8) return launch_mma<E4M3, D, 1, 8, 2, 1>(a, s);
+        if (a.pass_rows == 16) return launch_mma<E4M3, D, 2, 8, 2, 1>(a, s);
+        return launch_mma<E4M3, D, 4, 8, 2, 1>(a, s);
+    }
 }
 
 }  // namespace
@@ -764,8 +854,8 @@ int paged_pass_rows(int dtype, int rows) {
 cudaError_t launch_paged_attn(const PagedArgs &a, cudaStream_t s) {
     if (a.dtype == SKV_F32)
         return a.format == SKV_CACHE_E4M3 ? launch_simple<float, true>(a, s) : launch_simple<float, false>(a, s);
-    if (a.format == SKV_CACHE_E4M3) return a.d == 128 ? launch_rows<true, 128, 8, 5>(a, s) : launch_rows<true, 64, 8, 8>(a, s);
-    return a.d == 128 ? launch_rows<false, 128, 8, 2>(a, s) : launch_rows<false, 64, 8, 4>(a, s);
+    if (a.format == SKV_CACHE_E4M3) return a.d == 128 ? launch_rows<true, 128>(a, s) : launch_rows<true, 64>(a, s);
+    return a.d == 128 ? launch_rows<false, 128>(a, s) : launch_rows<false, 64>(a, s);
 }
 
 }  // namespace skv

@@ -247,6 +247,7 @@ struct PagedArgs {
     void *out;
     float *lse;
     int B, R, Hq, Hkv, G, d, dtype, format;
+    float inv_G;                         // 1 / G
     int rows;                            // R * G query rows per KV head
     int pass_rows, passes;               // rows one pass over the keys serves, ceil(rows / pass_rows)
     int ncta;

@@ -80,16 +80,29 @@ struct ChunkValues {
 //
 // A unit is one (sequence, KV head, pass over at most PASS query rows). Its keys [lo, hi) are cut
 // into rounds of RG token groups (one CTA-wide step); a unit without keys keeps one empty round, so
-// that it is scheduled and writes its outputs like the others. All rounds of all units, in order,
-// are dealt to the CTAs in equal contiguous ranges; a unit that a range end cuts is joined by the CTA
-// that finishes its last piece, in the order of the pieces, so that the result does not depend on
-// which CTA that is.
+// that it is scheduled and writes its outputs like the others. A unit weighs its rounds and COST more
+// (its query rows' load and its outputs take about as long as that many rounds). The weights of all
+// units, in order, are dealt to the CTAs in equal contiguous ranges; a unit that a range end cuts is
+// joined by the CTA that finishes its last piece, in the order of the pieces, so that the result
+// does not depend on which CTA that is.
 // ---------------------------------------------------------------------------
+constexpr int kPieceTable = 32;   // pieces of a CTA's range that are laid out at once
+
+struct PagedPiece {
+    int b, h, pass;
+    int r0, r1, rounds;   // rounds [r0, r1) of the unit's; r1 = r0: the range cuts only the unit's fixed weight
+    int lo, hi;           // the sequence's keys
+    int c0, np;           // CTA of the unit's first piece, pieces (1: this one is the whole unit)
+    // a unit's pieces but the first start their CTA's range, its first ends it
+    __device__ __forceinline__ int64_t slot(int cta) const { return 2 * static_cast<int64_t>(cta) + (r0 == 0 ? 1 : 0); }
+};
+
 struct PagedSched {
     int lo[SKV_MAX_SEQS], hi[SKV_MAX_SEQS];
-    int rounds[SKV_MAX_SEQS];            // rounds of one unit of the sequence
-    long long cum[SKV_MAX_SEQS + 1];     // rounds before the sequence (all its units)
+    long long cum[SKV_MAX_SEQS + 1];     // weight before the sequence (all its units)
     long long warp_sum[32];
+    PagedPiece piece[kPieceTable];
+    int unit0, n;                        // first unit of the range, pieces in the table
     int last;                            // this CTA completed the unit
 };
 
@@ -107,8 +120,14 @@ __device__ __forceinline__ void paged_range(const PagedArgs &a, int b, bool repo
     *hi = n;
 }
 
-// Fill the schedule (all threads of the CTA; ends with a barrier).
-template <int THREADS, int RG>
+template <int RG>
+__device__ __forceinline__ int paged_rounds(int lo, int hi) {
+    const int groups = (hi + kGroupTokens - 1) / kGroupTokens - lo / kGroupTokens;
+    return hi > lo ? (groups + RG - 1) / RG : 1;
+}
+
+// Weight before every sequence (all threads of the CTA; ends with a barrier).
+template <int THREADS, int RG, int COST>
 __device__ __forceinline__ void paged_schedule(const PagedArgs &a, PagedSched &s) {
     constexpr int PER = (SKV_MAX_SEQS + THREADS - 1) / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -121,17 +140,14 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs &a, PagedSched &s
         if (b < a.B) {
             int lo, hi;
             paged_range(a, b, blockIdx.x == 0, &lo, &hi);
-            const int g0 = lo / kGroupTokens, g1 = (hi + kGroupTokens - 1) / kGroupTokens;
-            const int r = hi > lo ? (g1 - g0 + RG - 1) / RG : 1;
             s.lo[b] = lo;
             s.hi[b] = hi;
-            s.rounds[b] = r;
-            mine[i] = static_cast<long long>(r) * mult;
+            mine[i] = static_cast<long long>(paged_rounds<RG>(lo, hi) + COST) * mult;
         }
         sum += mine[i];
     }
     long long inc = sum;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const long long up = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += up;
@@ -139,6 +155,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs &a, PagedSched &s
     if (lane == 31) s.warp_sum[warp] = inc;
     __syncthreads();
     long long base = inc - sum;
+#pragma unroll 1
     for (int w = 0; w < warp; ++w) base += s.warp_sum[w];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -150,56 +167,70 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs &a, PagedSched &s
     __syncthreads();
 }
 
-// One piece of a unit: rounds [r0, r1) of unit (b, h, pass).
-struct PagedPiece {
-    int b, h, pass;
-    int r0, r1, rounds;
-    long long unit0;   // first round of the unit, counted over all units
-    bool whole;        // the piece is the whole unit
-};
-
-// A CTA's walk over its range of rounds.
-struct PagedWalk {
-    long long x, end, total;
-    int ctas;   // CTAs that get a range
-    int b;
-
-    __device__ __forceinline__ long long start_of(int c) const { return total * c / ctas; }
-    __device__ __forceinline__ int cta_of(long long round) const {
-        return static_cast<int>(((round + 1) * ctas - 1) / total);
-    }
-    __device__ __forceinline__ void begin(const PagedArgs &a, const PagedSched &s) {
-        total = s.cum[a.B];
-        ctas = total < a.ncta ? static_cast<int>(total) : a.ncta;
-        const int c = blockIdx.x;
-        x = c < ctas ? start_of(c) : 0;
-        end = c < ctas ? start_of(c + 1) : 0;
-        int l = 0, r = a.B;   // the sequence whose rounds hold x
-        while (r - l > 1) {
-            const int m = (l + r) >> 1;
-            if (s.cum[m] <= x) l = m;
-            else r = m;
+// Lay out pieces `from` .. `from` + 31 of this CTA's range (all threads; ends with a barrier; the caller
+// puts one in front where the table is still in use). One lane per unit. With less work than LEAST per CTA
+// fewer CTAs get a range: a unit's pieces are joined by one CTA, at a cost for each. A kernel runs this
+// code once or twice, so that it is kept short: instruction fetches, not arithmetic, are its time.
+template <int RG, int COST, int LEAST>
+__device__ __forceinline__ void paged_pieces(const PagedArgs &a, PagedSched &s, int from) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, mult = a.Hkv * a.passes;
+        const long long total = s.cum[a.B];
+        const int ctas = static_cast<int>(min(static_cast<long long>(a.ncta), max(1ll, total / LEAST)));
+        // lanes 0 and 1: this CTA's range
+        const int c = blockIdx.x + (lane & 1);
+        const long long edge = c <= ctas ? total * c / ctas : total;
+        const long long x0 = __shfl_sync(0xffffffffu, edge, 0), x1 = __shfl_sync(0xffffffffu, edge, 1);
+        if (from == 0) {
+            int l = 0, r = a.B;   // the sequence whose weight holds x0
+            while (r - l > 1) {
+                const int m = (l + r) >> 1;
+                if (s.cum[m] <= x0) l = m;
+                else r = m;
+            }
+            const int wt = paged_rounds<RG>(s.lo[l], s.hi[l]) + COST;
+            if (lane == 0) s.unit0 = l * mult + static_cast<int>(x0 - s.cum[l]) / wt;   // one sequence's weight: host-checked
         }
-        b = l;
+        __syncwarp();
+        const int u = s.unit0 + from + lane, b = u / mult;
+        bool in = false;
+        if (b < a.B && x0 < x1) {
+            const int m = u - b * mult, lo = s.lo[b], hi = s.hi[b];
+            const int rounds = paged_rounds<RG>(lo, hi), wt = rounds + COST;
+            const long long at = s.cum[b] + static_cast<long long>(m) * wt;   // where the unit's weight starts
+            in = at < x1;
+            if (in) {
+                PagedPiece p;
+                p.b = b;
+                p.h = m / a.passes;
+                p.pass = m - p.h * a.passes;
+                p.rounds = rounds;
+                p.lo = lo;
+                p.hi = hi;
+                p.r0 = max(static_cast<int>(max(x0 - at, 0ll)) - COST, 0);
+                p.r1 = max(static_cast<int>(min(x1 - at, static_cast<long long>(wt))) - COST, 0);
+                p.c0 = blockIdx.x;
+                p.np = 1;
+                if (p.r0 > 0 || p.r1 < rounds) {
+                    // CTA of weight w: the largest c with total c / ctas (rounded down) <= w
+                    const long long w0 = at + COST, w1 = at + wt - 1;
+                    p.c0 = static_cast<int>(((w0 + 1) * ctas - 1) / total);
+                    p.np = static_cast<int>(((w1 + 1) * ctas - 1) / total) - p.c0 + 1;
+                }
+                s.piece[lane] = p;
+            }
+        }
+        const uint32_t have = __ballot_sync(0xffffffffu, in);
+        if (lane == 0) s.n = __popc(have);
     }
-    __device__ __forceinline__ bool next(const PagedArgs &a, const PagedSched &s, PagedPiece *p) {
-        if (x >= end) return false;
-        while (s.cum[b + 1] <= x) ++b;
-        const int r = s.rounds[b];
-        const int rem = static_cast<int>(x - s.cum[b]);   // < rounds x heads x passes of one sequence: checked on the host
-        const int m = rem / r;
-        p->b = b;
-        p->h = m / a.passes;
-        p->pass = m - p->h * a.passes;
-        p->rounds = r;
-        p->r0 = rem - m * r;
-        p->unit0 = x - p->r0;
-        p->r1 = end - x < r - p->r0 ? p->r0 + static_cast<int>(end - x) : r;
-        p->whole = p->r0 == 0 && p->r1 == r;
-        x += p->r1 - p->r0;
-        return true;
-    }
-};
+    __syncthreads();
+}
+
+// The next piece of the table at or after i that has rounds (s.n: none).
+__device__ __forceinline__ int paged_next(const PagedSched &s, int i) {
+    while (i < s.n && s.piece[i].r1 <= s.piece[i].r0) ++i;
+    return i;
+}
 
 // ---------------------------------------------------------------------------
 // attention: outputs and the join of a unit's pieces
@@ -219,76 +250,96 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
 // at most 1, so that neither partition can overflow.
 template <typename T, int D>
 __device__ __forceinline__ void paged_write(const PagedArgs &a, int b, int h, int row, int d0, float4 o, float l2) {
-    const int rr = row / a.G, g = row - rr * a.G;
+    const int rr = static_cast<int>((row + 0.5f) * a.inv_G), g = row - rr * a.G;   // row / G: exact below 2^22
     const int64_t r = (static_cast<int64_t>(b) * a.R + rr) * a.Hq + static_cast<int64_t>(h) * a.G + g;
     T *out = static_cast<T *>(a.out) + r * D + d0;
     if (a.prior_lse) {
         const float p2 = a.prior_lse[r] * 1.44269504088896340736f;
         if (p2 != -INFINITY) {   // a prior without weight is not read
             const float top = fmaxf(l2, p2);
-            const float w = exp2f(l2 - top), u = exp2f(p2 - top);
-            const float inv = 1.0f / (w + u);
+            const float w = ex2(l2 - top), u = ex2(p2 - top), sum = w + u;   // 1 <= sum <= 2
+            const float inv = __frcp_rn(sum), wi = w * inv, ui = u * inv;
             const float4 p = load4(static_cast<const T *>(a.prior_out) + r * D + d0);
-            o.x = (w * o.x + u * p.x) * inv;
-            o.y = (w * o.y + u * p.y) * inv;
-            o.z = (w * o.z + u * p.z) * inv;
-            o.w = (w * o.w + u * p.w) * inv;
-            l2 = top + log2f(w + u);
+            o = make_float4(wi * o.x + ui * p.x, wi * o.y + ui * p.y, wi * o.z + ui * p.z, wi * o.w + ui * p.w);
+            l2 = top + __log2f(sum);
         }
     }
     store4(out, o);
     if (d0 == 0) a.lse[r] = l2 * 0.69314718055994530942f;
 }
 
-// Join the pieces of one unit (in their order) and write its outputs. All threads of the CTA.
+// Join the pieces of one unit and write its outputs. All threads of the CTA. First the pieces' weights,
+// 2^(l - largest l) over their sum, into `scratch` (rows x (pieces + 1) words, one warp per row and one
+// round trip for 32 pieces); then each thread sums four outputs of a row over the pieces, AHEAD loads in
+// flight. The order of the sum is that of the pieces, whichever CTA this is.
 template <typename T, int D, int PASS, int THREADS>
-__device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedWalk &w, const PagedPiece &p) {
-    const int c0 = w.cta_of(p.unit0), c1 = w.cta_of(p.unit0 + p.rounds - 1);
-    const int slot0 = 2 * c0 + (w.start_of(c0) == p.unit0 ? 0 : 1);   // the others start their CTA's range
-    const int rows = min(PASS, a.rows - p.pass * PASS);
+__device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedPiece &p, float *scratch) {
+    constexpr int AHEAD = 8;
+    const int lane = threadIdx.x & 31, c0 = p.c0, np = p.np, row0 = p.pass * PASS;
+    const int rows = min(PASS, a.rows - row0);
+    const auto slot = [&](int k, int row) { return (2 * static_cast<int64_t>(c0 + k) + (k == 0 ? 1 : 0)) * PASS + row; };
+    float *parts = scratch + rows * np;   // the rows' log2 partitions
+#pragma unroll 1
+    for (int row = threadIdx.x >> 5; row < rows; row += THREADS / 32) {
+        float *wt = scratch + row * np;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int k = lane; k < np; k += 32) {
+            wt[k] = __ldcg(a.part_l + slot(k, row));
+            top = fmaxf(top, wt[k]);
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        top = top > -INFINITY ? top : 0.f;   // no piece with a key: every weight is 2^-inf = 0
+#pragma unroll 1
+        for (int k = lane; k < np; k += 32) sum += wt[k] = ex2(wt[k] - top);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);
+#pragma unroll 1
+        for (int k = lane; k < np; k += 32) wt[k] *= inv;
+        if (lane == 0) parts[row] = sum == 0.f ? -INFINITY : top + __log2f(sum);
+    }
+    __syncthreads();
+#pragma unroll 1
     for (int i = threadIdx.x; i < rows * (D / 4); i += THREADS) {
         const int row = i / (D / 4), d0 = (i % (D / 4)) * 4;
-        float top = -INFINITY;
-        for (int c = c0; c <= c1; ++c)
-            top = fmaxf(top, __ldcg(a.part_l + static_cast<int64_t>(c == c0 ? slot0 : 2 * c) * PASS + row));
-        top = top > -INFINITY ? top : 0.f;   // no piece with a key: every weight is 2^-inf = 0
+        const float *wt = scratch + row * np;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const int64_t slot = static_cast<int64_t>(c == c0 ? slot0 : 2 * c) * PASS + row;
-            const float f = exp2f(__ldcg(a.part_l + slot) - top);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot * D + d0));
-            sum += f;
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
-            o.z = fmaf(f, v.z, o.z);
-            o.w = fmaf(f, v.w, o.w);
+#pragma unroll 1
+        for (int k = 0; k < np; k += AHEAD) {
+            float4 v[AHEAD];
+#pragma unroll
+            for (int e = 0; e < AHEAD; ++e)
+                v[e] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot(min(k + e, np - 1), row) * D + d0));
+#pragma unroll
+            for (int e = 0; e < AHEAD; ++e) {
+                const float f = k + e < np ? wt[k + e] : 0.f;
+                o = make_float4(fmaf(f, v[e].x, o.x), fmaf(f, v[e].y, o.y), fmaf(f, v[e].z, o.z), fmaf(f, v[e].w, o.w));
+            }
         }
-        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        paged_write<T, D>(a, p.b, p.h, p.pass * PASS + row, d0, o, sum == 0.f ? -INFINITY : top + log2f(sum));
+        paged_write<T, D>(a, p.b, p.h, row0 + row, d0, o, parts[row]);
     }
 }
 
 // Count this CTA's piece of the unit; the CTA that counts the last one joins them. All threads
 // of the CTA, after its partial is written.
 template <typename T, int D, int PASS, int THREADS>
-__device__ __forceinline__ void paged_finish_piece(const PagedArgs &a, const PagedWalk &w, const PagedPiece &p,
-                                                   PagedSched &s) {
+__device__ __forceinline__ void paged_finish_piece(const PagedArgs &a, const PagedPiece &p, PagedSched &s, float *scratch) {
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-        const int pieces = w.cta_of(p.unit0 + p.rounds - 1) - w.cta_of(p.unit0) + 1;
         int *counter = a.counters + (static_cast<int64_t>(p.b) * a.Hkv + p.h) * a.passes + p.pass;
-        const bool last = atomicAdd(counter, 1) == pieces - 1;
+        const bool last = atomicAdd(counter, 1) == p.np - 1;
         if (last) *counter = 0;   // ready for the next call
         s.last = last;
         __threadfence();
     }
     __syncthreads();
-    if (s.last) paged_join<T, D, PASS, THREADS>(a, w, p);
-    __syncthreads();
+    if (s.last) {
+        paged_join<T, D, PASS, THREADS>(a, p, scratch);
+        __syncthreads();
+    }
 }
 
 }  // namespace skv
