@@ -36,6 +36,9 @@ bool pool_ok(const skv_token_cache *c) {
     return c && c->pages && aligned(c->pages, 16) && c->num_pages >= 0 && c->num_pages <= INT32_MAX;
 }
 
+// Vectors are read 16 bytes at a time. A dimension of one element has no stride that matters.
+bool stride_ok(int64_t stride, int64_t n, int64_t elem) { return stride >= 0 && (n <= 1 || stride * elem % 16 == 0); }
+
 bool overlap(const void *a, const void *b, size_t bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + bytes && y < x + bytes;
@@ -87,9 +90,9 @@ skv_status skv_cache_append(const void *k, const void *v, skv_dtype dtype, int64
     if (n_tokens < 0 || (!cu_new && n_tokens % B != 0)) return SKV_ERR_INVALID_ARG;
     if ((n_tokens > 0 && (!k || !v)) || !page_table || !lens || !new_lens || !pool_ok(cache)) return SKV_ERR_INVALID_ARG;
     const int64_t elem = dtype == SKV_BF16 ? 2 : 4;
-    const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
-    for (int64_t x : strides)
-        if (x < 0 || x * elem % 16 != 0) return SKV_ERR_INVALID_ARG;
+    if (!stride_ok(k_token_stride, n_tokens, elem) || !stride_ok(k_head_stride, Hkv, elem) ||
+        !stride_ok(v_token_stride, n_tokens, elem) || !stride_ok(v_head_stride, Hkv, elem))
+        return SKV_ERR_INVALID_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(new_lens, 4))
         return SKV_ERR_INVALID_ARG;
     // new_lens may be lens itself, and nothing in between
@@ -179,9 +182,8 @@ skv_status skv_paged_attn(const void *q, skv_dtype dtype, int64_t q_seq_stride, 
     if (st != SKV_OK) return st;
     if (!q || !page_table || !lens || !out || !lse || !pool_ok(cache)) return SKV_ERR_INVALID_ARG;
     const int64_t elem = dtype == SKV_BF16 ? 2 : 4;
-    const int64_t strides[3] = {q_seq_stride, q_row_stride, q_head_stride};
-    for (int64_t x : strides)
-        if (x < 0 || x * elem % 16 != 0) return SKV_ERR_INVALID_ARG;
+    if (!stride_ok(q_seq_stride, B, elem) || !stride_ok(q_row_stride, R, elem) || !stride_ok(q_head_stride, Hq, elem))
+        return SKV_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(lens, 4))
         return SKV_ERR_INVALID_ARG;
     a.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));

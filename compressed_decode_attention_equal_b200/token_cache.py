@@ -11,8 +11,8 @@ one launch on the current stream of the tensors' device (or on `stream`). There 
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -21,7 +21,6 @@ from ._lib import CACHE_GROUP_TOKENS, CACHE_PAGE_TOKENS, SkvError
 
 FORMATS = {"raw": _lib.SKV_CACHE_RAW, "e4m3": _lib.SKV_CACHE_E4M3}
 _DTYPES = {torch.bfloat16: _lib.SKV_BF16, torch.float32: _lib.SKV_F32}
-_NULL_SCOPE = contextlib.nullcontext()
 
 
 def token_pages_for(T: int) -> int:
@@ -72,7 +71,7 @@ class TokenCache:
             pages = torch.zeros(self.num_pages, self.page_bytes, dtype=torch.uint8, device=device)
         if pages.dtype != torch.uint8 or tuple(pages.shape) != (self.num_pages, self.page_bytes) or not pages.is_contiguous():
             raise ValueError(f"pages must be contiguous uint8 [{self.num_pages}, {self.page_bytes}]")
-        self.pages = pages
+        self.pages, self.device, self.on_gpu = pages, pages.device, pages.is_cuda
         p = pages.view(self.num_pages, self.Hkv, CACHE_PAGE_TOKENS // G, group)
         held = torch.float8_e4m3fn if e4m3 else dtype
         shape = (*p.shape[:3], G, self.d)
@@ -88,62 +87,74 @@ class TokenCache:
 
 
 # ---------------------------------------------------------------------------
-# argument checks shared by the three calls
+# Argument checks shared by the three calls. A decode step makes these calls for every layer, and a call
+# of few tokens takes less time on the GPU than its checks do here: each is a handful of attribute reads on the
+# way through, and says what is wrong only once something is.
 # ---------------------------------------------------------------------------
-def _check(t, name: str, device: torch.device, dtype: torch.dtype, shape: tuple) -> int:
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of current_stream()'s time
+
+
+def _stream_handle(device: torch.device) -> int:
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _ptr(t, name: str, device: torch.device, dtype: torch.dtype, shape) -> int:
     """Device pointer of a contiguous tensor of this device, type and shape."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{name} must be {dtype} {list(shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}")
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _check_table(table, cache: TokenCache, device: torch.device, B: int) -> int:
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B:
+def _vector_ptr(t, name: str, cache: TokenCache, dims: int) -> int:
+    """Device pointer of keys, values or queries: any strides, d contiguous."""
+    if t.dtype is not cache.dtype or t.device != cache.device or t.dim() != dims or t.stride(-1) != 1:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != cache.device:
+            raise ValueError(f"{name} must be on {cache.device}")
+        if t.dim() != dims or t.dtype is not cache.dtype:
+            raise ValueError(f"{name} must have {dims} dimensions and the cache's dtype")
+        raise ValueError(f"{name} must be contiguous along d")
+    return t.data_ptr()
+
+
+def _table_ptr(table, B: int, cache: TokenCache):
+    """Device pointer of the page table and its pages per sequence."""
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != B:
         raise ValueError("page_table must be int32 [B, max_pages]")
-    if cache.pages.device != device:
-        raise ValueError(f"cache must be on {device}")
-    return _check(table, "page_table", device, torch.int32, table.shape)
+    return _ptr(table, "page_table", cache.device, torch.int32, shape), shape[1]
 
 
-def _check_workspace(ws, device: torch.device, size: int):
-    """The given workspace's pointer and size, or a zeroed one of `size` bytes."""
+def _workspace(ws, device: torch.device, size: int):
+    """The given workspace, or a zeroed one of `size` bytes."""
     if ws is None:
-        ws = torch.zeros(size, dtype=torch.uint8, device=device)
-    elif not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        return torch.zeros(size, dtype=torch.uint8, device=device)
+    if ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
         raise ValueError(f"workspace must be contiguous uint8 on {device}")
-    return ws, ws.data_ptr(), ws.numel()
+    return ws
 
 
-def _scope(device: torch.device, stream):
-    """Where the launch and everything it allocates belongs: the tensors' device, and `stream`."""
+def _scoped(call, cache: TokenCache, stream, *args):
+    """Run `call` where its launch and all it allocates belong: on the cache's device, and on `stream`."""
+    device = cache.device
+    if not cache.on_gpu:
+        raise ValueError("the cache's pages must be a CUDA tensor")
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream must be on {device}")
-        return torch.cuda.stream(stream)
+        with torch.cuda.stream(stream):
+            return call(*args)
     if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return _NULL_SCOPE
-
-
-def _vectors(t, name: str, dims: int, cache: TokenCache) -> torch.device:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != dims or t.shape[-1] != cache.d or t.dtype != cache.dtype:
-        raise ValueError(f"{name} must have {dims} dimensions and the cache's dtype and d")
-    if t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous along d")
-    return t.device
-
-
-def _strides(t: torch.Tensor, dims: int):
-    """Strides of the leading dimensions; one of a single element has none that matters."""
-    return [st if n > 1 else 0 for st, n in zip(t.stride()[:dims], t.shape)]
+        with torch.cuda.device(device):
+            return call(*args)
+    return call(*args)
 
 
 # ---------------------------------------------------------------------------
@@ -158,33 +169,39 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, cache: TokenCache, page_table
     page_table: int32 [B, max_pages], naming the pages of the new positions too. Returns the new lengths:
     new_lens if given (it may be lens: updated in place), else a new tensor. workspace: at least 256
     bytes of uint8, zeroed once (workspace_error() reads its error flags)."""
-    device = _vectors(k, "k", 3, cache)
-    if _vectors(v, "v", 3, cache) != device or v.shape != k.shape:
-        raise ValueError("k and v must have the same shape and device")
-    n, Hkv, d = k.shape
-    if Hkv != cache.Hkv:
-        raise ValueError("k and v must have the cache's Hkv heads")
-    B = lens.shape[0] if isinstance(lens, torch.Tensor) and lens.dim() == 1 else 0
-    if B < 1:
+    return _scoped(_append, cache, stream, k, v, cache, page_table, lens, cu_new, new_lens, workspace)
+
+
+def _append(k, v, cache, page_table, lens, cu_new, new_lens, workspace):
+    device = cache.device
+    k_p, v_p = _vector_ptr(k, "k", cache, 3), _vector_ptr(v, "v", cache, 3)
+    shape = k.shape
+    n, Hkv, d = shape
+    if v.shape != shape or Hkv != cache.Hkv or d != cache.d:
+        raise ValueError("k and v must be [n, Hkv, d] of the cache's Hkv and d")
+    per_seq = lens.shape
+    if len(per_seq) != 1 or per_seq[0] < 1:
         raise ValueError("lens must be int32 [B]")
-    lens_p = _check(lens, "lens", device, torch.int32, (B,))
-    table_p = _check_table(page_table, cache, device, B)
+    B = per_seq[0]
+    lens_p = _ptr(lens, "lens", device, torch.int32, per_seq)
+    table_p, max_pages = _table_ptr(page_table, B, cache)
     if cu_new is not None:
-        cu_p = _check(cu_new, "cu_new", device, torch.int32, (B + 1,))
+        cu_p = _ptr(cu_new, "cu_new", device, torch.int32, (B + 1,))
     elif n % B != 0:
         raise ValueError("without cu_new the rows of k must divide evenly among the sequences")
     else:
         cu_p = None
-    (kt, kh), (vt, vh) = _strides(k, 2), _strides(v, 2)
-    with _scope(device, stream):
-        if new_lens is None:
-            new_lens = torch.empty_like(lens)
-        new_p = _check(new_lens, "new_lens", device, torch.int32, (B,))
-        workspace, ws_p, ws_n = _check_workspace(workspace, device, 256)
-        _lib.check(_lib.load().skv_cache_append(
-            k.data_ptr(), v.data_ptr(), cache._dtype_code, kt, kh, vt, vh, B, Hkv, d, n, cu_p, cache._format_code,
-            cache._ref, table_p, page_table.shape[1], lens_p, new_p, ws_p, ws_n,
-            torch.cuda.current_stream(device).cuda_stream), "skv_cache_append")
+    if new_lens is None:
+        new_lens = torch.empty_like(lens)
+    new_p = lens_p if new_lens is lens else _ptr(new_lens, "new_lens", device, torch.int32, per_seq)
+    ws = _workspace(workspace, device, 256)
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    st = _lib.load().skv_cache_append(k_p, v_p, cache._dtype_code, kt, kh, vt, vh, B, Hkv, d, n, cu_p, cache._format_code,
+                                      cache._ref, table_p, max_pages, lens_p, new_p, ws.data_ptr(), ws.numel(),
+                                      _stream_handle(device))
+    if st:
+        raise SkvError(st, "skv_cache_append")
     return new_lens
 
 
@@ -193,25 +210,36 @@ def cache_read(cache: TokenCache, page_table: torch.Tensor, first_list, T_list, 
     """Read positions first_list[b] .. first_list[b] + T_list[b] - 1 of every sequence (host lists) into k, v
     [sum_b Hkv * T_b, d] of the cache's dtype, sequence b a contiguous [Hkv, T_b, d] block: what coarsen() takes.
     Returns (k, v)."""
-    B = len(T_list)
+    return _scoped(_read, cache, stream, cache, page_table, first_list, T_list, k, v, workspace)
+
+
+def _read(cache, page_table, first_list, T_list, k, v, workspace):
+    device, B = cache.device, len(T_list)
     if len(first_list) != B or B < 1:
         raise ValueError("first_list and T_list must name the same sequences, at least one")
-    device = cache.pages.device
-    table_p = _check_table(page_table, cache, device, B)
-    rows = (cache.Hkv * sum(int(t) for t in T_list), cache.d)
+    table_p, max_pages = _table_ptr(page_table, B, cache)
+    ints = _int_arrays(B)
+    T = ints(*T_list)
+    rows = (cache.Hkv * sum(T), cache.d)
     if rows[0] < 0:
         raise ValueError("T_list must not be negative")
-    ints = ctypes.c_int32 * B
-    with _scope(device, stream):
-        k = torch.empty(rows, dtype=cache.dtype, device=device) if k is None else k
-        v = torch.empty(rows, dtype=cache.dtype, device=device) if v is None else v
-        k_p, v_p = (_check(t, name, device, cache.dtype, rows) for t, name in ((k, "k"), (v, "v")))
-        workspace, ws_p, ws_n = _check_workspace(workspace, device, 256)
-        _lib.check(_lib.load().skv_cache_read(
-            cache._ref, cache._dtype_code, cache._format_code, B, cache.Hkv, cache.d, ints(*map(int, first_list)),
-            ints(*map(int, T_list)), table_p, page_table.shape[1], k_p, v_p, ws_p, ws_n,
-            torch.cuda.current_stream(device).cuda_stream), "skv_cache_read")
+    if k is None:
+        k = torch.empty(rows, dtype=cache.dtype, device=device)
+    if v is None:
+        v = torch.empty(rows, dtype=cache.dtype, device=device)
+    k_p, v_p = _ptr(k, "k", device, cache.dtype, rows), _ptr(v, "v", device, cache.dtype, rows)
+    ws = _workspace(workspace, device, 256)
+    st = _lib.load().skv_cache_read(cache._ref, cache._dtype_code, cache._format_code, B, cache.Hkv, cache.d,
+                                    ints(*first_list), T, table_p, max_pages, k_p, v_p, ws.data_ptr(), ws.numel(),
+                                    _stream_handle(device))
+    if st:
+        raise SkvError(st, "skv_cache_read")
     return k, v
+
+
+@functools.lru_cache(maxsize=None)
+def _int_arrays(n: int):
+    return ctypes.c_int32 * n
 
 
 def paged_attn_workspace_bytes(B: int, R: int, Hq: int, Hkv: int, d: int, max_pages: int) -> int:
@@ -229,34 +257,47 @@ def paged_attn(q: torch.Tensor, cache: TokenCache, page_table: torch.Tensor, len
     tokens before `first`; the result is then that of one attention over all keys (out may be prior's out, lse
     not prior's lse). A row without keys gives out 0, lse -inf. workspace: paged_attn_workspace_bytes bytes of
     uint8, zeroed once. Returns (out [B, R, Hq, d], lse [B, R, Hq] fp32)."""
-    device = _vectors(q, "q", 4, cache)
-    B, R, Hq, d = q.shape
-    lens_p = _check(lens, "lens", device, torch.int32, (B,))
-    table_p = _check_table(page_table, cache, device, B)
-    qs = _strides(q, 3)
-    opts = _lib.SkvPagedAttnOptions(0.0 if scale is None else scale, softcap, window)
-    if scale is not None and scale == 0.0:
-        raise ValueError("scale must not be zero")
-    if first is not None:
-        opts.first = _check(first, "first", device, torch.int32, (B,))
-    if slopes is not None:
-        opts.slopes = _check(slopes, "slopes", device, torch.float32, (Hq,))
-    if prior is not None:
-        opts.prior_out = _check(prior[0], "prior out", device, q.dtype, (B, R, Hq, d))
-        opts.prior_lse = _check(prior[1], "prior lse", device, torch.float32, (B, R, Hq))
-    with _scope(device, stream):
-        if out is None:
-            out = torch.empty(B, R, Hq, d, dtype=q.dtype, device=device)
-        if lse is None:
-            lse = torch.empty(B, R, Hq, dtype=torch.float32, device=device)
-        out_p = _check(out, "out", device, q.dtype, (B, R, Hq, d))
-        lse_p = _check(lse, "lse", device, torch.float32, (B, R, Hq))
-        if workspace is None:
-            size = paged_attn_workspace_bytes(B, R, Hq, cache.Hkv, d, page_table.shape[1])
-            workspace = torch.zeros(max(size, 256), dtype=torch.uint8, device=device)
-        workspace, ws_p, ws_n = _check_workspace(workspace, device, 256)
-        _lib.check(_lib.load().skv_paged_attn(
-            q.data_ptr(), cache._dtype_code, qs[0], qs[1], qs[2], B, R, Hq, cache.Hkv, d, cache._format_code, cache._ref,
-            table_p, page_table.shape[1], lens_p, out_p, lse_p, ws_p, ws_n, ctypes.byref(opts),
-            torch.cuda.current_stream(device).cuda_stream), "skv_paged_attn")
+    return _scoped(_attn, cache, stream, q, cache, page_table, lens, first, window, scale, softcap, slopes, prior, out,
+                   lse, workspace)
+
+
+def _attn(q, cache, page_table, lens, first, window, scale, softcap, slopes, prior, out, lse, workspace):
+    device = cache.device
+    q_p = _vector_ptr(q, "q", cache, 4)
+    shape = q.shape
+    B, R, Hq, d = shape
+    if d != cache.d:
+        raise ValueError("q must have the cache's d")
+    lens_p = _ptr(lens, "lens", device, torch.int32, (B,))
+    table_p, max_pages = _table_ptr(page_table, B, cache)
+    rows = shape[:3]
+    opts = None
+    if scale is not None or softcap or window or first is not None or slopes is not None or prior is not None:
+        if scale == 0.0:
+            raise ValueError("scale must not be zero")
+        opts = _lib.SkvPagedAttnOptions(0.0 if scale is None else scale, softcap, window)
+        if first is not None:
+            opts.first = _ptr(first, "first", device, torch.int32, (B,))
+        if slopes is not None:
+            opts.slopes = _ptr(slopes, "slopes", device, torch.float32, (Hq,))
+        if prior is not None:
+            opts.prior_out = _ptr(prior[0], "prior out", device, q.dtype, shape)
+            opts.prior_lse = _ptr(prior[1], "prior lse", device, torch.float32, rows)
+        opts = ctypes.byref(opts)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=device)
+    if lse is None:
+        lse = torch.empty(rows, dtype=torch.float32, device=device)
+    out_p = _ptr(out, "out", device, q.dtype, shape)
+    lse_p = _ptr(lse, "lse", device, torch.float32, rows)
+    if workspace is None:
+        size = paged_attn_workspace_bytes(B, R, Hq, cache.Hkv, d, max_pages)
+        workspace = torch.zeros(max(size, 256), dtype=torch.uint8, device=device)
+    ws = _workspace(workspace, device, 256)
+    qb, qr, qh, _ = q.stride()
+    st = _lib.load().skv_paged_attn(q_p, cache._dtype_code, qb, qr, qh, B, R, Hq, cache.Hkv, d, cache._format_code, cache._ref,
+                                    table_p, max_pages, lens_p, out_p, lse_p, ws.data_ptr(), ws.numel(), opts,
+                                    _stream_handle(device))
+    if st:
+        raise SkvError(st, "skv_paged_attn")
     return out, lse

@@ -431,7 +431,8 @@ size_t skv_cache_page_bytes(skv_dtype dtype, skv_cache_format format, int Hkv, i
  * Append tokens, quantising them on the way (SKV_CACHE_E4M3).
  *
  * k, v      : [n_tokens][Hkv][d] in dtype, d contiguous; token and head strides in elements (slices
- *             of a fused projection need no copy). 16-byte aligned, strides multiples of 16 bytes.
+ *             of a fused projection need no copy). 16-byte aligned, strides multiples of 16 bytes (that of a
+ *             dimension of one element is not looked at).
  * cu_new    : [B + 1] int32 device: rows cu_new[b] .. cu_new[b + 1] - 1 are sequence b's new tokens
  *             (0 <= cu_new[b] <= cu_new[b + 1] <= n_tokens). Rows outside are ignored. NULL: every
  *             sequence gets n_tokens / B tokens (n_tokens a multiple of B).
@@ -496,7 +497,7 @@ size_t skv_paged_attn_workspace_bytes(int B, int R, int Hq, int Hkv, int d, int 
  * Attention of the new token over the exact-token cache.
  *
  * q     : R query rows per sequence, q[b][r][hq] at element b q_seq_stride + r q_row_stride + hq
- *         q_head_stride, d contiguous, in dtype; 16-byte aligned, strides multiples of 16 bytes. The
+ *         q_head_stride, d contiguous, in dtype; aligned as skv_cache_append's k. The
  *         rows are independent (as skv_decode_attn's): each stands at the last position lens[b] - 1
  *         and sees every key there is. Query head hq reads KV head hq / (Hq / Hkv).
  * s_j = scale q.k_j (capped, biased) over the keys j in [max(first, lens - window), lens);
