@@ -336,6 +336,86 @@ struct Feeder {
     }
 };
 
+// One warp's ring of S stages, a token group each: copies are issued S groups ahead of the computation, one
+// bulk copy per group, and across piece ends. A group on a bad page is reported and skipped. When a wait
+// gives up the warp issues and waits for nothing more (bar the copies in flight, at the end).
+template <int W, int S, int BYTES, int STAGE>
+struct GroupRing {
+    uint8_t *buf;           // [S][STAGE]
+    uint64_t *full;         // [S]
+    Feeder<W> feed;
+    uint32_t skip;          // stages whose group's page id is bad: nothing was copied
+    uint32_t pending;       // stages with a copy that has not been waited for
+    uint32_t phase;
+    int stage;
+    bool dead;
+
+    __device__ __forceinline__ void init(uint8_t *ring, uint64_t *bars) {
+        buf = ring;
+        full = bars;
+        skip = pending = phase = 0;
+        stage = 0;
+        dead = false;
+        if ((threadIdx.x & 31) == 0) {
+            for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void issue(const PagedArgs &a, const PagedSched &sched, int s) {
+        if (feed.i >= sched.n || dead) return;
+        const bool leader = (threadIdx.x & 31) == 0;
+        const int page = feed.page();
+        if (page < 0 || page >= a.num_pages) {
+            if (leader) {
+                raise_flag(a.flags, FLAG_BAD_PAGE);
+                mbar_arrive(&full[s]);
+            }
+            skip |= 1u << s;
+        } else {
+            skip &= ~(1u << s);
+            if (leader) {
+                const int64_t group = (static_cast<int64_t>(page) * a.Hkv + sched.piece[feed.i].h) * kPageGroups + feed.g % kPageGroups;
+                mbar_arrive_expect_tx(&full[s], BYTES);
+                bulk_g2s(buf + s * STAGE, a.pages + group * BYTES, BYTES, &full[s]);
+            }
+        }
+        pending |= 1u << s;
+        feed.step(a, sched, threadIdx.x >> 5);
+    }
+    // a new piece table: nothing is in flight
+    __device__ __forceinline__ void begin(const PagedArgs &a, const PagedSched &sched) {
+        feed.i = 0;
+        feed.settle(a, sched, threadIdx.x >> 5);
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) issue(a, sched, stage + s < S ? stage + s : stage + s - S);
+    }
+    // false: nothing to compute (a wait gave up; the stage stays)
+    __device__ __forceinline__ bool wait(const PagedArgs &a) {
+        if (!dead && !mbar_wait(&full[stage], phase)) {
+            dead = true;
+            if ((threadIdx.x & 31) == 0) raise_flag(a.flags, FLAG_TIMEOUT);
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        if (!dead) pending &= ~(1u << stage);
+        return !dead;
+    }
+    __device__ __forceinline__ bool skipped() const { return skip >> stage & 1; }
+    __device__ __forceinline__ const uint8_t *data() const { return buf + stage * STAGE; }
+    // every lane is done with the stage: copy the next group there, go on to the next stage
+    __device__ __forceinline__ void release(const PagedArgs &a, const PagedSched &sched) {
+        __syncwarp();
+        issue(a, sched, stage);
+        if (++stage == S) stage = 0, phase ^= 1;
+    }
+    // a warp that gave up leaves only when the copies that it issued have landed (bounded again)
+    __device__ __forceinline__ void drain() {
+        if (dead)
+            for (int s = 0; s < S; ++s)
+                if (pending >> s & 1) mbar_wait(&full[s], s < stage ? phase ^ 1 : phase);
+    }
+};
+
 // k_paged_mma (bf16 queries): mma.sync m16n8k16 with the tokens as M and 8 NT query rows as N, so that
 // a group of up to 8 query heads reads every key once and the logits' accumulators, after one 8x8
 // transpose per tile, are the second product's operand. HBM bounds it: a key and value are 258
@@ -363,42 +443,13 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Sm &sm = *reinterpret_cast<Sm *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
-    if (lane == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(&sm.full[warp][s], 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
+    GroupRing<W, S, G::kGroup, Sm::kStage> ring;
+    ring.init(sm.ring[warp][0], sm.full[warp]);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     paged_schedule<THREADS, W, Sm::kCost>(a, sm.sched);
     paged_pieces<W, Sm::kCost, Sm::kLeast>(a, sm.sched, 0);
 
-    const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * kPageGroups * G::kGroup;
-    uint32_t skip = 0;      // stages whose group's page id is bad: nothing was copied
-    uint32_t pending = 0;   // stages with a copy that has not been waited for
-    bool dead = false;      // a wait gave up: no further copies, no further waits
-    Feeder<W> feed{};
-    const auto issue = [&](int s) {
-        if (feed.i >= sm.sched.n || dead) return;
-        const int page = feed.page();
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0) {
-                raise_flag(a.flags, FLAG_BAD_PAGE);
-                mbar_arrive(&sm.full[warp][s]);
-            }
-            skip |= 1u << s;
-        } else {
-            skip &= ~(1u << s);
-            if (lane == 0) {
-                const uint8_t *src = a.pages + page * page_bytes +
-                                     (static_cast<int64_t>(sm.sched.piece[feed.i].h) * kPageGroups + feed.g % kPageGroups) * G::kGroup;
-                mbar_arrive_expect_tx(&sm.full[warp][s], G::kGroup);
-                bulk_g2s(sm.ring[warp][s], src, G::kGroup, &sm.full[warp][s]);
-            }
-        }
-        pending |= 1u << s;
-        feed.step(a, sm.sched, warp);
-    };
     constexpr int PER = D / 32, RPW = (ROWS + W - 1) / W;   // query elements per lane and row, rows per warp
     uint32_t qx[RPW][PER / 2];
     float qslope[RPW];
@@ -425,8 +476,6 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
         }
     };
     const float cap_l2 = a.softcap * kLog2e;
-    int stage = 0;
-    uint32_t phase = 0;
     int from = 0, at = paged_next(sm.sched, 0);
     bool fresh = true;   // a new table: nothing is ahead
 #pragma unroll 1
@@ -443,10 +492,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
         const PagedPiece &pc = sm.sched.piece[at];
         if (fresh) {   // the queries' loads before anything waits, then the ring
             load_queries(pc);
-            feed.i = 0;
-            feed.settle(a, sm.sched, warp);
-#pragma unroll 1
-            for (int s = 0; s < S; ++s) issue(stage + s < S ? stage + s : stage + s - S);
+            ring.begin(a, sm.sched);
             fresh = false;
         }
         const int row0 = pc.pass * ROWS, rows = min(ROWS, a.rows - row0);
@@ -509,16 +555,10 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
         }
 #pragma unroll 1
         for (int gi = g0 + pc.r0 * W + warp; gi < g_end; gi += W) {
-            if (!dead && !mbar_wait(&sm.full[warp][stage], phase)) {
-                dead = true;
-                if (lane == 0) raise_flag(a.flags, FLAG_TIMEOUT);
-            }
-            dead = __any_sync(0xffffffffu, dead);
-            if (dead) continue;
+            if (!ring.wait(a)) continue;
             {
-                pending &= ~(1u << stage);
-                if (!(skip >> stage & 1)) {
-                    const uint8_t *buf = sm.ring[warp][stage];
+                if (!ring.skipped()) {
+                    const uint8_t *buf = ring.data();
                     const uint32_t base = smem_u32(buf);
                     const int t0 = gi * kGroupTokens;
                     // ---- logits: tokens g, g + 8 x rows 2 tq, 2 tq + 1 of every tile
@@ -679,10 +719,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                         }
                     }
                 }
-                __syncwarp();   // every lane has read the stage
-                issue(stage);
+                ring.release(a, sm.sched);
             }
-            if (++stage == S) stage = 0, phase ^= 1;
         }
         const int after = paged_next(sm.sched, at + 1);
         if (after < sm.sched.n) load_queries(sm.sched.piece[after]);   // they arrive while the warps join
@@ -760,10 +798,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
         if (pc.np > 1) paged_finish_piece<__nv_bfloat16, D, ROWS, THREADS>(a, pc, sm.sched, sm.o);
         at = after;
     }
-    // a warp that gave up leaves only when the copies that it issued have landed (bounded again)
-    if (dead)
-        for (int s = 0; s < S; ++s)
-            if (pending >> s & 1) mbar_wait(&sm.full[warp][s], s < stage ? phase ^ 1 : phase);
+    ring.drain();
 }
 
 // CTAs of a kernel that fit the current device at once (kept per kernel and device in a fixed table:

@@ -151,7 +151,7 @@ __device__ __forceinline__ void quantise(const uint32_t (&w)[W], int e, uint32_t
 }
 
 template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 5) k_cache_append(const AppendArgs a) {
+__global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_cache_append(const AppendArgs a) {
     using G = CacheGeom<T, E4M3, D>;
     constexpr int N = D / 16;                     // elements per lane
     constexpr int W = N * static_cast<int>(sizeof(T)) / 4;
