@@ -1,11 +1,9 @@
 // skv_paged_attn: attention of the new token's query rows over the exact-token cache.
 //
-// k_paged_f32 (fp32 caches and queries): CUDA cores, exact fp32 products. A warp takes 32 tokens:
-// for the logits each lane owns one token and walks its key chunk by chunk against up to 8 query rows
-// broadcast from shared memory (32 FMAs per 16-byte key load and 8 broadcast loads); for the values
-// the lanes own dimensions, so that a value row is one coalesced load, with the 8 weights of the
-// token broadcast. Each warp keeps its own running maximum, sum and outputs; the CTA's eight join
-// at the end of a piece.
+// One launch: every CTA takes an equal share of the token groups of all (sequence, KV head) units, its warps
+// stream the groups through private rings of bulk copies and keep their own running maximum, sum and outputs;
+// they join at the end of a unit's piece, and the CTA that ends a unit's last piece joins the pieces. Two
+// kernels on that frame: k_paged_mma (bf16 queries, tensor cores) and k_paged_f32 (fp32 queries, exact fp32 FMAs).
 #include <mutex>
 
 #include "token_cache.cuh"
@@ -26,224 +24,6 @@ __device__ __forceinline__ float capped(float t, float cap) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(t * (2.0f * kLog2e)) + 1.0f));
     return fmaf(-2.0f * cap, r, cap);
-}
-
-constexpr int kSimpleWarps = 8, kSimpleThreads = 32 * kSimpleWarps, kSimplePass = 8;
-constexpr int kSimpleRound = 2 * kSimpleWarps;   // token groups of a round: 32 tokens per warp
-constexpr int kSimpleCost = 1;
-constexpr int kSimpleMaxCtas = 480;              // the join keeps a word per row and piece where the outputs are
-
-template <int D>
-struct SimpleSmem {
-    PagedSched sched;
-    alignas(16) float q[kSimplePass][D];
-    float p[kSimpleWarps][32][kSimplePass];
-    float o[kSimpleWarps][kSimplePass][D];
-    float m[kSimpleWarps][kSimplePass], l[kSimpleWarps][kSimplePass];
-};
-
-template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(kSimpleThreads) k_paged_f32(const PagedArgs a) {
-    using G = CacheGeom<T, E4M3, D>;
-    using CV = ChunkValues<T, E4M3>;
-    constexpr int NR = kSimplePass, PER = D / 32;   // PER output dimensions per lane
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    SimpleSmem<D> &sm = *reinterpret_cast<SimpleSmem<D> *>(smem_raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    paged_schedule<kSimpleThreads, kSimpleRound, kSimpleCost>(a, sm.sched);
-    paged_pieces<kSimpleRound, kSimpleCost, 1>(a, sm.sched, 0);
-    const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * kPageGroups * G::kGroup;
-    const T *q = static_cast<const T *>(a.q);
-    for (int from = 0, i = 0;; ++i) {
-        i = paged_next(sm.sched, i);
-        if (i == sm.sched.n) {
-            if (i < kPieceTable) break;
-            __syncthreads();
-            from += kPieceTable;
-            paged_pieces<kSimpleRound, kSimpleCost, 1>(a, sm.sched, from);
-            i = -1;
-            continue;
-        }
-        const PagedPiece pc = sm.sched.piece[i];
-        const int row0 = pc.pass * NR, rows = min(NR, a.rows - row0);
-        for (int e = tid; e < NR * D; e += kSimpleThreads) {
-            const int r = e / D, d = e % D;
-            float x = 0.f;
-            if (r < rows) {
-                const int rr = (row0 + r) / a.G, g = (row0 + r) % a.G;
-                x = static_cast<float>(q[pc.b * a.q_b + rr * a.q_r + (static_cast<int64_t>(pc.h) * a.G + g) * a.q_h + d]);
-            }
-            sm.q[r][d] = x;
-        }
-        float slope[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-            slope[r] = a.slopes && r < rows ? a.slopes[pc.h * a.G + (row0 + r) % a.G] : 0.f;
-        __syncthreads();
-        const int lo = pc.lo, hi = pc.hi, g0 = lo / kGroupTokens;
-        const int t_end = min(hi, (g0 + pc.r1 * kSimpleRound) * kGroupTokens);
-        float m[NR], l[NR], o[NR][PER];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) o[r][i] = 0.f;
-        }
-        for (int t0 = (g0 + pc.r0 * kSimpleRound) * kGroupTokens + 32 * warp; t0 < t_end; t0 += 32 * kSimpleWarps) {
-            // logits: lane = token
-            const int t = t0 + lane;
-            bool valid = t >= lo && t < t_end;
-            const uint8_t *grp = nullptr;
-            if (valid) {
-                const int page = a.page_table[static_cast<int64_t>(pc.b) * a.max_pages + t / SKV_CACHE_PAGE_TOKENS];
-                if (page < 0 || page >= a.num_pages) {
-                    raise_flag(a.flags, FLAG_BAD_PAGE);
-                    valid = false;
-                } else {
-                    grp = a.pages + page * page_bytes +
-                          (static_cast<int64_t>(pc.h) * kPageGroups + t % SKV_CACHE_PAGE_TOKENS / kGroupTokens) * G::kGroup;
-                }
-            }
-            const int n = t % kGroupTokens;
-            float s[NR];
-#pragma unroll
-            for (int r = 0; r < NR; ++r) s[r] = 0.f;
-            float vs = 1.f;
-            if (valid) {
-                const uint8_t *key = grp + n * G::kVec;
-                constexpr int AHEAD = G::kChunks < 8 ? G::kChunks : 8;   // loads in flight per lane
-#pragma unroll 1
-                for (int c0 = 0; c0 < G::kChunks; c0 += AHEAD) {
-                  uint4 raw[AHEAD];
-#pragma unroll
-                  for (int e = 0; e < AHEAD; ++e)
-                      raw[e] = *reinterpret_cast<const uint4 *>(key + 16 * cache_chunk(c0 + e, n, G::kChunks));
-#pragma unroll
-                  for (int e = 0; e < AHEAD; ++e) {
-                    const int c = c0 + e;
-                    float x[CV::N];
-                    CV::get(raw[e], x);
-#pragma unroll
-                    for (int r = 0; r < NR; ++r)
-#pragma unroll
-                        for (int i = 0; i < CV::N; i += 4) {
-                            const float4 y = *reinterpret_cast<const float4 *>(&sm.q[r][c * CV::N + i]);
-                            s[r] = fmaf(x[i], y.x, s[r]);
-                            s[r] = fmaf(x[i + 1], y.y, s[r]);
-                            s[r] = fmaf(x[i + 2], y.z, s[r]);
-                            s[r] = fmaf(x[i + 3], y.w, s[r]);
-                        }
-                  }
-                }
-                float ks = a.scale;
-                if constexpr (E4M3) {
-                    ks *= scale_of(grp[2 * G::kBlock + n]);
-                    vs = scale_of(grp[2 * G::kBlock + kGroupTokens + n]);
-                }
-                const float gap = static_cast<float>(hi - 1 - t);
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    s[r] *= ks;
-                    if (a.softcap > 0.f) s[r] = capped_exact(s[r] / a.softcap, a.softcap);
-                    s[r] = (s[r] - slope[r] * gap) * kLog2e;
-                }
-            } else {
-#pragma unroll
-                for (int r = 0; r < NR; ++r) s[r] = -INFINITY;
-            }
-            // running maximum and sum (each lane keeps the sum of its own tokens)
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                float top = s[r];
-#pragma unroll
-                for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                top = fmaxf(top, m[r]);
-                const float f = top > -INFINITY ? exp2f(m[r] - top) : 1.f;
-                const float p = top > -INFINITY || s[r] != s[r] ? exp2f(s[r] - top) : 0.f;
-                m[r] = top;
-                l[r] = l[r] * f + p;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) o[r][i] *= f;
-                sm.p[warp][lane][r] = p * vs;
-            }
-            __syncwarp();
-            // values: lane = dimensions
-            const uint32_t mask = __ballot_sync(0xffffffffu, valid);
-            const uint64_t base = reinterpret_cast<uint64_t>(grp);
-#pragma unroll 16
-            for (int j = 0; j < 32; ++j) {
-                if (!(mask >> j & 1)) continue;   // masked rows are not read: they may hold anything
-                const uint8_t *g = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, base, j));
-                const int nj = (t0 + j) % kGroupTokens;
-                const int byte = lane * PER * G::kElem;
-                const uint8_t *vp = g + G::kBlock + nj * G::kVec + 16 * cache_chunk(byte / 16, nj, G::kChunks) + byte % 16;
-                float x[PER];
-                if constexpr (E4M3) {
-                    const uint16_t w0 = *reinterpret_cast<const unsigned short *>(vp);
-                    const float2 f0 = f16x2_to_f32(e4m3x2_to_f16x2(w0));
-                    x[0] = f0.x, x[1] = f0.y;
-                    if constexpr (PER == 4) {
-                        const float2 f1 = f16x2_to_f32(
-                            e4m3x2_to_f16x2(*reinterpret_cast<const unsigned short *>(vp + 2)));
-                        x[2] = f1.x, x[3] = f1.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) x[i] = static_cast<float>(reinterpret_cast<const T *>(vp)[i]);
-                }
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const float p = sm.p[warp][j][r];
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) o[r][i] = fmaf(p, x[i], o[r][i]);
-                }
-            }
-            __syncwarp();
-        }
-        // join the warps
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            float sum = l[r];
-#pragma unroll
-            for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            if (lane == 0) sm.m[warp][r] = m[r], sm.l[warp][r] = sum;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) sm.o[warp][r][lane * PER + i] = o[r][i];
-        }
-        __syncthreads();
-        for (int i = tid; i < rows * (D / 4); i += kSimpleThreads) {
-            const int r = i / (D / 4), d0 = (i % (D / 4)) * 4;
-            float top = -INFINITY;
-            for (int w = 0; w < kSimpleWarps; ++w) top = fmaxf(top, sm.m[w][r]);
-            top = top > -INFINITY ? top : 0.f;
-            float sum = 0.f;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < kSimpleWarps; ++w) {
-                const float f = exp2f(sm.m[w][r] - top);
-                sum += f * sm.l[w][r];
-                const float4 y = load4(&sm.o[w][r][d0]);
-                x.x = fmaf(f, y.x, x.x);
-                x.y = fmaf(f, y.y, x.y);
-                x.z = fmaf(f, y.z, x.z);
-                x.w = fmaf(f, y.w, x.w);
-            }
-            const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-            x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-            const float l2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-            if (pc.np == 1) {
-                paged_write<T, D>(a, pc.b, pc.h, row0 + r, d0, x, l2);
-            } else {
-                const int64_t slot = pc.slot(blockIdx.x) * NR + r;
-                store4(a.part_o + slot * D + d0, x);
-                if (d0 == 0) a.part_l[slot] = l2;
-            }
-        }
-        if (pc.np == 1) __syncthreads();
-        else paged_finish_piece<T, D, NR, kSimpleThreads>(a, pc, sm.sched, &sm.o[0][0][0]);
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -801,6 +581,266 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
     ring.drain();
 }
 
+// ---------------------------------------------------------------------------
+// fp32 queries: CUDA cores
+// ---------------------------------------------------------------------------
+// k_paged_f32: exact fp32 products on packed FMAs, out of the same rings. For the logits a lane takes tokens
+// n, n + 8 and rows r, r + 4 over all of d (16 FMAs to four 16-byte loads, both operands shared by neighbouring
+// lanes); for the outputs it takes d / 32 dimensions of all 8 rows (one load of its values per token and the
+// 8 weights broadcast). HBM bounds raw caches at d = 128: 16 KB per group are 712 clocks of one SM, the
+// group's ~1,400 instructions 350.
+constexpr int kF32Rows = 8;
+
+template <bool E4M3, int D, int W, int S>
+struct F32Smem {
+    using G = CacheGeom<float, E4M3, D>;
+    static constexpr int kStage = (G::kGroup + 127) / 128 * 128;
+    static constexpr int kMaxCtas = 160;             // the join of a unit's pieces keeps a word per row and piece in o
+    static constexpr int kCost = 2, kLeast = 2;
+    static constexpr int kOut = W * kF32Rows * D, kJoin = kF32Rows * (kMaxCtas + 1);
+    alignas(128) uint8_t ring[W][S][kStage];
+    alignas(16) float o[kOut > kJoin ? kOut : kJoin];   // [W][rows][D]
+    alignas(16) float q[kF32Rows][D + 4];
+    alignas(16) float p[W][kGroupTokens][kF32Rows];     // a group's weights (times the values' scales)
+    alignas(16) float f[W][kF32Rows];                   // what the outputs are rescaled by
+    float slope[kF32Rows];
+    float m[W][kF32Rows], l[W][kF32Rows], part[kF32Rows];
+    alignas(8) uint64_t full[W][S];
+    PagedSched sched;
+};
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+template <bool E4M3, int D, int W, int S>
+__global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
+    using Sm = F32Smem<E4M3, D, W, S>;
+    using G = typename Sm::G;
+    using CV = ChunkValues<float, E4M3>;
+    constexpr int NR = kF32Rows, PER = D / 32, THREADS = 32 * W;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Sm &sm = *reinterpret_cast<Sm *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tq = lane & 7, rg = lane >> 3;
+    GroupRing<W, S, G::kGroup, Sm::kStage> ring;
+    ring.init(sm.ring[warp][0], sm.full[warp]);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    paged_schedule<THREADS, W, Sm::kCost>(a, sm.sched);
+    paged_pieces<W, Sm::kCost, Sm::kLeast>(a, sm.sched, 0);
+    int from = 0, at = paged_next(sm.sched, 0);
+    bool fresh = true;   // a new table: nothing is ahead
+#pragma unroll 1
+    while (true) {
+        if (at == sm.sched.n) {
+            if (at < kPieceTable) break;
+            __syncthreads();
+            from += kPieceTable;
+            paged_pieces<W, Sm::kCost, Sm::kLeast>(a, sm.sched, from);
+            at = paged_next(sm.sched, 0);
+            fresh = true;
+            continue;
+        }
+        const PagedPiece &pc = sm.sched.piece[at];
+        if (fresh) {
+            ring.begin(a, sm.sched);
+            fresh = false;
+        }
+        const int row0 = pc.pass * NR, rows = min(NR, a.rows - row0);
+        for (int i = tid; i < NR * (D / 4); i += THREADS) {
+            const int r = i / (D / 4), d0 = (i % (D / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            float slope = 0.f;
+            if (r < rows) {
+                const int rr = static_cast<int>((row0 + r + 0.5f) * a.inv_G), hq = pc.h * a.G + row0 + r - rr * a.G;
+                x = load4(static_cast<const float *>(a.q) + pc.b * a.q_b + rr * a.q_r + hq * a.q_h + d0);
+                if (a.slopes && d0 == 0) slope = a.slopes[hq];
+            }
+            store4(&sm.q[r][d0], x);
+            if (d0 == 0) sm.slope[r] = slope;
+        }
+        __syncthreads();
+        const int lo = pc.lo, hi = pc.hi, g0 = lo / kGroupTokens;
+        const int g_end = hi > lo ? min((hi + kGroupTokens - 1) / kGroupTokens, g0 + pc.r1 * W) : 0;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        uint64_t o[PER][NR / 2];   // row pairs
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+            for (int r = 0; r < NR / 2; ++r) o[i][r] = 0;
+#pragma unroll 1
+        for (int gi = g0 + pc.r0 * W + warp; gi < g_end; gi += W) {
+            if (!ring.wait(a)) continue;
+            if (!ring.skipped()) {
+                const uint8_t *buf = ring.data();
+                const int t0 = gi * kGroupTokens;
+                // ---- logits: tokens tq, tq + 8 x rows rg, rg + 4
+                uint64_t acc[2][2] = {};
+                const uint8_t *key = buf + tq * G::kVec;
+#pragma unroll 4
+                for (int c = 0; c < G::kChunks; ++c) {
+                    float x[2][CV::N];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        CV::get(*reinterpret_cast<const uint4 *>(key + 8 * t * G::kVec + 16 * cache_chunk(c, tq, G::kChunks)), x[t]);
+#pragma unroll
+                    for (int i = 0; i < CV::N; i += 4)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float4 y = load4(&sm.q[rg + 4 * r][c * CV::N + i]);
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                acc[t][r] = ffma2(f2pack(x[t][i], x[t][i + 1]), f2pack(y.x, y.y), acc[t][r]);
+                                acc[t][r] = ffma2(f2pack(x[t][i + 2], x[t][i + 3]), f2pack(y.z, y.w), acc[t][r]);
+                            }
+                        }
+                }
+                float s[2][2], vs[2] = {1.f, 1.f};
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int n = tq + 8 * t;
+                    float ks = a.scale;
+                    if constexpr (E4M3) {
+                        ks *= scale_of(buf[2 * G::kBlock + n]);
+                        vs[t] = scale_of(buf[2 * G::kBlock + kGroupTokens + n]);
+                    }
+                    const bool in = t0 + n >= lo && t0 + n < hi;
+                    const float gap = static_cast<float>(hi - 1 - t0 - n);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float x, y;
+                        f2unpack(acc[t][r], x, y);
+                        float z = (x + y) * ks;
+                        if (a.softcap > 0.f) z = capped_exact(z / a.softcap, a.softcap);
+                        s[t][r] = in ? (z - sm.slope[rg + 4 * r] * gap) * kLog2e : -INFINITY;
+                    }
+                }
+                // ---- running maximum and sum (each lane keeps the sum of its own tokens)
+                bool moved = false;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float top = fmaxf(s[0][r], s[1][r]);
+#pragma unroll
+                    for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    top = fmaxf(top, m[r]);
+                    const float ref = top > -INFINITY ? top : 0.f;   // no key yet: weights 2^-inf = 0
+                    const float f = ex2(m[r] - ref);
+                    moved |= f != 1.f;
+                    m[r] = top;
+                    l[r] *= f;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const float p = ex2(s[t][r] - ref);
+                        l[r] += p;
+                        sm.p[warp][tq + 8 * t][rg + 4 * r] = p * vs[t];
+                    }
+                    if (tq == 0) sm.f[warp][rg + 4 * r] = f;
+                }
+                moved = __any_sync(0xffffffffu, moved);
+                __syncwarp();
+                if (moved) {
+                    const uint64_t *f = reinterpret_cast<const uint64_t *>(sm.f[warp]);
+#pragma unroll
+                    for (int r = 0; r < NR / 2; ++r)
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) o[i][r] = mul2(o[i][r], f[r]);
+                }
+                // ---- outputs: dimensions lane PER .. of the tokens that are seen (others may hold anything)
+                const int n0 = max(lo - t0, 0), n1 = min(hi - t0, kGroupTokens);
+                constexpr int bytes = PER * G::kElem;
+#pragma unroll 4
+                for (int n = n0; n < n1; ++n) {
+                    const uint8_t *vp = buf + G::kBlock + n * G::kVec + 16 * cache_chunk(lane * bytes / 16, n, G::kChunks) + lane * bytes % 16;
+                    float x[PER];
+                    if constexpr (E4M3) {
+                        const float2 f0 = f16x2_to_f32(e4m3x2_to_f16x2(*reinterpret_cast<const unsigned short *>(vp)));
+                        x[0] = f0.x, x[1] = f0.y;
+                        if constexpr (PER == 4) {
+                            const float2 f1 = f16x2_to_f32(e4m3x2_to_f16x2(*reinterpret_cast<const unsigned short *>(vp + 2)));
+                            x[2] = f1.x, x[3] = f1.y;
+                        }
+                    } else if constexpr (PER == 4) {
+                        const float4 u = *reinterpret_cast<const float4 *>(vp);
+                        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+                    } else {
+                        const float2 u = *reinterpret_cast<const float2 *>(vp);
+                        x[0] = u.x, x[1] = u.y;
+                    }
+                    const ulonglong2 p01 = *reinterpret_cast<const ulonglong2 *>(&sm.p[warp][n][0]);
+                    const ulonglong2 p23 = *reinterpret_cast<const ulonglong2 *>(&sm.p[warp][n][4]);
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const uint64_t v = f2pack(x[i], x[i]);
+                        o[i][0] = ffma2(p01.x, v, o[i][0]);
+                        o[i][1] = ffma2(p01.y, v, o[i][1]);
+                        o[i][2] = ffma2(p23.x, v, o[i][2]);
+                        o[i][3] = ffma2(p23.y, v, o[i][3]);
+                    }
+                }
+            }
+            ring.release(a, sm.sched);
+        }
+        // ---- join the warps; those that had no group have nothing to add
+        const int act = max(1, min(W, g_end - (g0 + pc.r0 * W)));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float sum = l[r];
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            if (tq == 0) sm.m[warp][rg + 4 * r] = m[r], sm.l[warp][rg + 4 * r] = sum;
+        }
+#pragma unroll
+        for (int r = 0; r < NR / 2; ++r)
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                float x, y;
+                f2unpack(o[i][r], x, y);
+                sm.o[(warp * NR + 2 * r) * D + lane * PER + i] = x;
+                sm.o[(warp * NR + 2 * r + 1) * D + lane * PER + i] = y;
+            }
+        __syncthreads();
+        static_assert((W & (W - 1)) == 0, "one lane per row and warp");
+        if (tid < NR * W) {   // the warps' weights, 2^(m - largest m) over the joint sum, and the row's partition
+            const int r = tid / W, w = tid % W;
+            const float mine = sm.m[w][r];
+            float top = mine;
+#pragma unroll
+            for (int x = 1; x < W; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            top = top > -INFINITY ? top : 0.f;
+            const float f = ex2(mine - top);
+            float sum = f * sm.l[w][r];
+#pragma unroll
+            for (int x = 1; x < W; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            sm.m[w][r] = sum == 0.f ? 0.f : f * __frcp_rn(sum);
+            if (w == 0) sm.part[r] = sum == 0.f ? -INFINITY : top + __log2f(sum);
+        }
+        __syncthreads();
+        for (int i = tid; i < rows * (D / 4); i += THREADS) {
+            const int r = i / (D / 4), d0 = (i % (D / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = 0; w < act; ++w) {
+                const float f = sm.m[w][r];
+                const float4 y = load4(&sm.o[(w * NR + r) * D + d0]);
+                x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
+            }
+            if (pc.np == 1) {
+                paged_write<float, D>(a, pc.b, pc.h, row0 + r, d0, x, sm.part[r]);
+            } else {
+                const int64_t to = pc.slot(blockIdx.x) * NR + r;
+                store4(a.part_o + to * D + d0, x);
+                if (d0 == 0) a.part_l[to] = sm.part[r];
+            }
+        }
+        __syncthreads();
+        if (pc.np > 1) paged_finish_piece<float, D, NR, THREADS>(a, pc, sm.sched, sm.o);
+        at = paged_next(sm.sched, at + 1);
+    }
+    ring.drain();
+}
+
 // CTAs of a kernel that fit the current device at once (kept per kernel and device in a fixed table:
 // nothing here allocates or throws).
 struct GridEntry {
@@ -852,12 +892,9 @@ cudaError_t launch(K kernel, const PagedArgs &a0, int threads, size_t smem, int 
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <typename T, bool E4M3>
-cudaError_t launch_simple(const PagedArgs &a, cudaStream_t s) {
-    if (a.d == 128) return launch(k_paged_f32<T, E4M3, 128>, a, kSimpleThreads, sizeof(SimpleSmem<128>),
-                  kSimpleMaxCtas, s);
-    return launch(k_paged_f32<T, E4M3, 64>, a, kSimpleThreads, sizeof(SimpleSmem<64>),
-                  kSimpleMaxCtas, s);
+template <bool E4M3, int D, int W, int S>
+cudaError_t launch_f32(const PagedArgs &a, cudaStream_t s) {
+    return launch(k_paged_f32<E4M3, D, W, S>, a, 32 * W, sizeof(F32Smem<E4M3, D, W, S>) + 128, F32Smem<E4M3, D, W, S>::kMaxCtas, s);
 }
 
 template <bool E4M3, int D, int NT, int W, int S, int CTAS>
@@ -882,13 +919,15 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
 }  // namespace
 
 int paged_pass_rows(int dtype, int rows) {
-    if (dtype == SKV_F32) return kSimplePass;
+    if (dtype == SKV_F32) return kF32Rows;
     return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 }
 
 cudaError_t launch_paged_attn(const PagedArgs &a, cudaStream_t s) {
-    if (a.dtype == SKV_F32)
-        return a.format == SKV_CACHE_E4M3 ? launch_simple<float, true>(a, s) : launch_simple<float, false>(a, s);
+    if (a.dtype == SKV_F32) {
+        if (a.format == SKV_CACHE_E4M3) return a.d == 128 ? launch_f32<true, 128, 8, 4>(a, s) : launch_f32<true, 64, 8, 4>(a, s);
+        return a.d == 128 ? launch_f32<false, 128, 4, 3>(a, s) : launch_f32<false, 64, 8, 2>(a, s);
+    }
     if (a.format == SKV_CACHE_E4M3) return a.d == 128 ? launch_rows<true, 128>(a, s) : launch_rows<true, 64>(a, s);
     return a.d == 128 ? launch_rows<false, 128>(a, s) : launch_rows<false, 64>(a, s);
 }
