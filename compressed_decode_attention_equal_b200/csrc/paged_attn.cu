@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
                 // ---- logits: tokens tq, tq + 8 x rows rg, rg + 4
                 uint64_t acc[2][2] = {};
                 const uint8_t *key = buf + tq * G::kVec;
-#pragma unroll 4
+#pragma unroll 8
                 for (int c = 0; c < G::kChunks; ++c) {
                     float x[2][CV::N];
 #pragma unroll
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
                 // ---- outputs: dimensions lane PER .. of the tokens that are seen (others may hold anything)
                 const int n0 = max(lo - t0, 0), n1 = min(hi - t0, kGroupTokens);
                 constexpr int bytes = PER * G::kElem;
-#pragma unroll 4
+#pragma unroll 8
                 for (int n = n0; n < n1; ++n) {
                     const uint8_t *vp = buf + G::kBlock + n * G::kVec + 16 * cache_chunk(lane * bytes / 16, n, G::kChunks) + lane * bytes % 16;
                     float x[PER];
@@ -926,7 +926,7 @@ int paged_pass_rows(int dtype, int rows) {
 cudaError_t launch_paged_attn(const PagedArgs &a, cudaStream_t s) {
     if (a.dtype == SKV_F32) {
         if (a.format == SKV_CACHE_E4M3) return a.d == 128 ? launch_f32<true, 128, 8, 4>(a, s) : launch_f32<true, 64, 8, 4>(a, s);
-        return a.d == 128 ? launch_f32<false, 128, 4, 3>(a, s) : launch_f32<false, 64, 8, 2>(a, s);
+        return a.d == 128 ? launch_f32<false, 128, 8, 1>(a, s) : launch_f32<false, 64, 8, 2>(a, s);
     }
     if (a.format == SKV_CACHE_E4M3) return a.d == 128 ? launch_rows<true, 128>(a, s) : launch_rows<true, 64>(a, s);
     return a.d == 128 ? launch_rows<false, 128>(a, s) : launch_rows<false, 64>(a, s);

@@ -195,7 +195,7 @@ struct AppendArgs {
     int B, Hkv, d, dtype, format;
     int n_tokens;
     int per_seq;                         // tokens per sequence when cu is null
-    int per_warp;                        // tokens that one warp takes
+    int per_warp;                        // steps that one warp takes
     const int32_t *cu;                   // [B + 1] offsets of the sequences' new tokens, or null
     uint8_t *pages;
     int64_t num_pages;

@@ -150,7 +150,9 @@ __device__ __forceinline__ void quantise(const uint32_t (&w)[W], int e, uint32_t
     }
 }
 
-template <typename T, bool E4M3, int D>
+// FLAT false: a step is kHeads heads of one token. FLAT true: kHeads consecutive (token, head) rows, whatever
+// their tokens; for head counts that kHeads does not divide, whose steps would be partly empty.
+template <typename T, bool E4M3, int D, bool FLAT>
 __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_cache_append(const AppendArgs a) {
     using G = CacheGeom<T, E4M3, D>;
     constexpr int N = D / 16;                     // elements per lane
@@ -158,26 +160,44 @@ __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-    // this warp: tokens i0 .. i0 + count - 1, heads h0 .. h0 + kHeads - 1
-    const unsigned chunks = (a.Hkv + kHeads - 1) / kHeads;
-    const unsigned item = blockIdx.x * kAppendWarps + (threadIdx.x >> 5), part = item / chunks;
-    const int h0 = static_cast<int>(item - part * chunks) * kHeads, heads = min(kHeads, a.Hkv - h0);
-    const int64_t i0 = static_cast<int64_t>(part) * a.per_warp;
-    const int count = static_cast<int>(max(min(static_cast<int64_t>(a.per_warp), a.n_tokens - i0), int64_t{0}));
-    const T *src = (half ? static_cast<const T *>(a.v) + i0 * a.v_token + h0 * a.v_head
-                         : static_cast<const T *>(a.k) + i0 * a.k_token + h0 * a.k_head) + l * N;
+    const unsigned item = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    // this warp: tokens i0 .. i0 + count - 1, heads h0 .. h0 + kHeads - 1; or (FLAT) rows i0 .. i0 + count - 1
+    int64_t i0;
+    int h0 = 0, count;
+    if constexpr (FLAT) {
+        i0 = static_cast<int64_t>(item) * (a.per_warp * kHeads);
+        count = static_cast<int>(max(min(static_cast<int64_t>(a.per_warp * kHeads), static_cast<int64_t>(a.n_tokens) * a.Hkv - i0), int64_t{0}));
+    } else {
+        const unsigned chunks = a.Hkv / kHeads, part = item / chunks;
+        h0 = static_cast<int>(item - part * chunks) * kHeads;
+        i0 = static_cast<int64_t>(part) * a.per_warp;
+        count = static_cast<int>(max(min(static_cast<int64_t>(a.per_warp), a.n_tokens - i0), int64_t{0}));
+    }
+    const int steps = FLAT ? (count + kHeads - 1) / kHeads : count;
+    // FLAT: lane r holds the token and head of row i0 + r
+    const int token = static_cast<int>(FLAT ? (i0 + lane) / a.Hkv : i0 + lane);
+    const int head = FLAT ? static_cast<int>(i0 + lane - static_cast<int64_t>(token) * a.Hkv) : h0;
+    const T *src = (half ? static_cast<const T *>(a.v) : static_cast<const T *>(a.k)) + l * N;
     const int64_t token_stride = half ? a.v_token : a.k_token, head_stride = half ? a.v_head : a.k_head;
-    const auto load_token = [&](int t, uint32_t (&w)[kHeads][W]) {
+    const auto load_step = [&](int t, uint32_t (&w)[kHeads][W]) {
+        if (t >= steps) return;
 #pragma unroll
-        for (int j = 0; j < kHeads; ++j)
-            if (t < count && j < heads) load_row<T, N>(src + t * token_stride + j * head_stride, w[j]);
+        for (int j = 0; j < kHeads; ++j) {
+            if constexpr (FLAT) {
+                const int r = t * kHeads + j;
+                const int64_t tk = __shfl_sync(0xffffffffu, token, r), hd = __shfl_sync(0xffffffffu, head, r);
+                if (r < count) load_row<T, N>(src + tk * token_stride + hd * head_stride, w[j]);
+            } else {
+                load_row<T, N>(src + (i0 + t) * token_stride + (h0 + j) * head_stride, w[j]);
+            }
+        }
     };
     uint32_t next[kHeads][W] = {};
-    load_token(0, next);
-    // lane t: where token i0 + t goes (page -1: nowhere)
+    load_step(0, next);
+    // lane t: where token (row) t goes (page -1: nowhere)
     int where_page = -1, where_slot = 0;
     if (lane < count) {
-        const int i = static_cast<int>(i0) + lane;
+        const int i = token;
         int b, off;
         bool ok = true;
         if (a.cu) {
@@ -238,25 +258,38 @@ __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_c
         }
     }
 #pragma unroll 1
-    for (int t = 0; t < count; ++t) {
+    for (int t = 0; t < steps; ++t) {
         uint32_t w[kHeads][W];
 #pragma unroll
         for (int j = 0; j < kHeads; ++j)
 #pragma unroll
             for (int q = 0; q < W; ++q) w[j][q] = next[j][q];
-        load_token(t + 1, next);
-        const int page = __shfl_sync(0xffffffffu, where_page, t), slot = __shfl_sync(0xffffffffu, where_slot, t);
-        if (page < 0) continue;
-        const int n = slot % kGroupTokens;
-        uint8_t *grp = a.pages + ((static_cast<int64_t>(page) * a.Hkv + h0) * kPageGroups + slot / kGroupTokens) * G::kGroup;
-        uint8_t *row = grp + half * G::kBlock + n * G::kVec;
-        uint8_t *exps = grp + 2 * G::kBlock + half * kGroupTokens + n;
+        load_step(t + 1, next);
+        int n = 0;
+        uint8_t *grp = nullptr;
+        if constexpr (!FLAT) {
+            const int page = __shfl_sync(0xffffffffu, where_page, t), slot = __shfl_sync(0xffffffffu, where_slot, t);
+            if (page < 0) continue;
+            n = slot % kGroupTokens;
+            grp = a.pages + ((static_cast<int64_t>(page) * a.Hkv + h0) * kPageGroups + slot / kGroupTokens) * G::kGroup;
+        }
         int e[kHeads];
         if constexpr (E4M3)
             if (!scale_exponents<T, W, false>(w, e)) scale_exponents<T, W, true>(w, e);
 #pragma unroll
-        for (int j = 0; j < kHeads; ++j, row += kPageGroups * G::kGroup, exps += kPageGroups * G::kGroup) {
-            if (j >= heads) break;
+        for (int j = 0; j < kHeads; ++j) {
+            if constexpr (FLAT) {
+                const int r = (t * kHeads + j) & 31;
+                const int page = __shfl_sync(0xffffffffu, where_page, r), slot = __shfl_sync(0xffffffffu, where_slot, r);
+                const int hd = __shfl_sync(0xffffffffu, head, r);
+                if (page < 0) continue;   // rows behind the last one among them
+                n = slot % kGroupTokens;
+                grp = a.pages + ((static_cast<int64_t>(page) * a.Hkv + hd) * kPageGroups + slot / kGroupTokens) * G::kGroup;
+            } else if (j > 0) {
+                grp += kPageGroups * G::kGroup;   // the next head
+            }
+            uint8_t *row = grp + half * G::kBlock + n * G::kVec;
+            uint8_t *exps = grp + 2 * G::kBlock + half * kGroupTokens + n;
             if constexpr (E4M3) {
                 uint32_t c[N / 4];
                 quantise<T, N, W>(w[j], e[j], c);
@@ -390,17 +423,26 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T, bool E4M3>
-cudaError_t append_t(const AppendArgs &a0, cudaStream_t s) {
+template <typename T, bool E4M3, int D>
+cudaError_t append_d(const AppendArgs &a0, cudaStream_t s) {
     AppendArgs a = a0;
-    // tokens of a warp: one while there are not enough warps for the GPU
-    const int64_t chunks = (a.Hkv + kHeads - 1) / kHeads;
-    const int64_t per = a.n_tokens * chunks / (148 * 32);
+    // Flat rows where a step of whole tokens would be partly empty: 74,211 tokens x 1 head 56.8 -> FLATNEW us; they cost
+    // two more shuffles and products per row (x 4 heads 40.9 -> FLATOLD us), so that other head counts do without.
+    const bool flat = a.Hkv % kHeads != 0;
+    const int64_t all = flat ? (static_cast<int64_t>(a.n_tokens) * a.Hkv + kHeads - 1) / kHeads : static_cast<int64_t>(a.n_tokens) * (a.Hkv / kHeads);
+    // steps of a warp: one while there are not enough warps for the GPU
+    const int64_t per = all / (148 * 32);
     a.per_warp = static_cast<int>(per < 1 ? 1 : per > kAppendTokens ? kAppendTokens : per);
-    const int64_t items = (a.n_tokens + a.per_warp - 1) / a.per_warp * chunks;
+    const int64_t items = flat ? (all + a.per_warp - 1) / a.per_warp
+                               : (a.n_tokens + a.per_warp - 1) / a.per_warp * static_cast<int64_t>(a.Hkv / kHeads);
     const int64_t grid = items > 0 ? (items + kAppendWarps - 1) / kAppendWarps : 1;   // the lengths are written at least
-    return a.d == 128 ? launch(k_cache_append<T, E4M3, 128>, grid, 32 * kAppendWarps, s, a)
-                      : launch(k_cache_append<T, E4M3, 64>, grid, 32 * kAppendWarps, s, a);
+    return flat ? launch(k_cache_append<T, E4M3, D, true>, grid, 32 * kAppendWarps, s, a)
+                : launch(k_cache_append<T, E4M3, D, false>, grid, 32 * kAppendWarps, s, a);
+}
+
+template <typename T, bool E4M3>
+cudaError_t append_t(const AppendArgs &a, cudaStream_t s) {
+    return a.d == 128 ? append_d<T, E4M3, 128>(a, s) : append_d<T, E4M3, 64>(a, s);
 }
 
 template <typename T, bool E4M3>
