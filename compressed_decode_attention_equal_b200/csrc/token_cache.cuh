@@ -79,7 +79,7 @@ struct ChunkValues {
 // attention: which CTA reads which tokens
 //
 // A unit is one (sequence, KV head, pass over at most PASS query rows). Its keys [lo, hi) are cut
-// into rounds of RG token groups (one CTA-wide step); a unit without keys keeps one empty round, so
+// into rounds of W tiles of TT tokens, one per warp; a unit without keys keeps one empty round, so
 // that it is scheduled and writes its outputs like the others. A unit weighs its rounds and COST more
 // (its query rows' load and its outputs take about as long as that many rounds). The weights of all
 // units, in order, are dealt to the CTAs in equal contiguous ranges; a unit that a range end cuts is
@@ -120,14 +120,14 @@ __device__ __forceinline__ void paged_range(const PagedArgs &a, int b, bool repo
     *hi = n;
 }
 
-template <int RG>
+template <int W, int TT>
 __device__ __forceinline__ int paged_rounds(int lo, int hi) {
-    const int groups = (hi + kGroupTokens - 1) / kGroupTokens - lo / kGroupTokens;
-    return hi > lo ? (groups + RG - 1) / RG : 1;
+    const int tiles = (hi + TT - 1) / TT - lo / TT;
+    return hi > lo ? (tiles + W - 1) / W : 1;
 }
 
 // Weight before every sequence (all threads of the CTA; ends with a barrier).
-template <int THREADS, int RG, int COST>
+template <int THREADS, int W, int TT, int COST>
 __device__ __forceinline__ void paged_schedule(const PagedArgs &a, PagedSched &s) {
     constexpr int PER = (SKV_MAX_SEQS + THREADS - 1) / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -142,7 +142,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs &a, PagedSched &s
             paged_range(a, b, blockIdx.x == 0, &lo, &hi);
             s.lo[b] = lo;
             s.hi[b] = hi;
-            mine[i] = static_cast<long long>(paged_rounds<RG>(lo, hi) + COST) * mult;
+            mine[i] = static_cast<long long>(paged_rounds<W, TT>(lo, hi) + COST) * mult;
         }
         sum += mine[i];
     }
@@ -171,7 +171,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs &a, PagedSched &s
 // puts one in front where the table is still in use). One lane per unit. With less work than LEAST per CTA
 // fewer CTAs get a range: a unit's pieces are joined by one CTA, at a cost for each. A kernel runs this
 // code once or twice, so that it is kept short: instruction fetches, not arithmetic, are its time.
-template <int RG, int COST, int LEAST>
+template <int W, int TT, int COST, int LEAST>
 __device__ __forceinline__ void paged_pieces(const PagedArgs &a, PagedSched &s, int from) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x, mult = a.Hkv * a.passes;
@@ -188,7 +188,7 @@ __device__ __forceinline__ void paged_pieces(const PagedArgs &a, PagedSched &s, 
                 if (s.cum[m] <= x0) l = m;
                 else r = m;
             }
-            const int wt = paged_rounds<RG>(s.lo[l], s.hi[l]) + COST;
+            const int wt = paged_rounds<W, TT>(s.lo[l], s.hi[l]) + COST;
             if (lane == 0) s.unit0 = l * mult + static_cast<int>(x0 - s.cum[l]) / wt;   // one sequence's weight: host-checked
         }
         __syncwarp();
@@ -196,7 +196,7 @@ __device__ __forceinline__ void paged_pieces(const PagedArgs &a, PagedSched &s, 
         bool in = false;
         if (b < a.B && x0 < x1) {
             const int m = u - b * mult, lo = s.lo[b], hi = s.hi[b];
-            const int rounds = paged_rounds<RG>(lo, hi), wt = rounds + COST;
+            const int rounds = paged_rounds<W, TT>(lo, hi), wt = rounds + COST;
             const long long at = s.cum[b] + static_cast<long long>(m) * wt;   // where the unit's weight starts
             in = at < x1;
             if (in) {
