@@ -218,11 +218,8 @@ def _read(cache, page_table, first_list, T_list, k, v, workspace):
     if len(first_list) != B or B < 1:
         raise ValueError("first_list and T_list must name the same sequences, at least one")
     table_p, max_pages = _table_ptr(page_table, B, cache)
-    ints = _int_arrays(B)
-    T = ints(*T_list)
+    T, first = _int32s(T_list, "T_list"), _int32s(first_list, "first_list")
     rows = (cache.Hkv * sum(T), cache.d)
-    if rows[0] < 0:
-        raise ValueError("T_list must not be negative")
     if k is None:
         k = torch.empty(rows, dtype=cache.dtype, device=device)
     if v is None:
@@ -230,7 +227,7 @@ def _read(cache, page_table, first_list, T_list, k, v, workspace):
     k_p, v_p = _ptr(k, "k", device, cache.dtype, rows), _ptr(v, "v", device, cache.dtype, rows)
     ws = _workspace(workspace, device, 256)
     st = _lib.load().skv_cache_read(cache._ref, cache._dtype_code, cache._format_code, B, cache.Hkv, cache.d,
-                                    ints(*first_list), T, table_p, max_pages, k_p, v_p, ws.data_ptr(), ws.numel(),
+                                    first, T, table_p, max_pages, k_p, v_p, ws.data_ptr(), ws.numel(),
                                     _stream_handle(device))
     if st:
         raise SkvError(st, "skv_cache_read")
@@ -238,8 +235,15 @@ def _read(cache, page_table, first_list, T_list, k, v, workspace):
 
 
 @functools.lru_cache(maxsize=None)
-def _int_arrays(n: int):
+def _int_array(n: int):
     return ctypes.c_int32 * n
+
+
+def _int32s(values, name: str):
+    """A C array of host integers (ctypes alone would cut them to 32 bits)."""
+    if not (0 <= min(values) and max(values) < 1 << 31):
+        raise ValueError(f"{name} must be integers from 0 to 2^31 - 1")
+    return _int_array(len(values))(*map(int, values))
 
 
 def paged_attn_workspace_bytes(B: int, R: int, Hq: int, Hkv: int, d: int, max_pages: int) -> int:
@@ -275,6 +279,8 @@ def _attn(q, cache, page_table, lens, first, window, scale, softcap, slopes, pri
     if scale is not None or softcap or window or first is not None or slopes is not None or prior is not None:
         if scale == 0.0:
             raise ValueError("scale must not be zero")
+        if not 0 <= window < 1 << 31:
+            raise ValueError("window must be from 0 to 2^31 - 1")
         opts = _lib.SkvPagedAttnOptions(0.0 if scale is None else scale, softcap, window)
         if first is not None:
             opts.first = _ptr(first, "first", device, torch.int32, (B,))

@@ -307,6 +307,43 @@ def test_attention_long_ragged_batch_and_determinism(fmt):
     ok(ws)
 
 
+@pytest.mark.parametrize("dtype,fmt", [(BF, "e4m3"), (BF, "raw"), (F32, "raw")])
+@pytest.mark.parametrize("d,B,Hkv,G", [(64, 260, 63, 1), (128, 512, 24, 1), (128, 150, 40, 20)])
+def test_attention_many_short_units(dtype, fmt, d, B, Hkv, G):
+    """Far more (sequence, head) units than CTAs, so that a CTA lays its pieces out several times over; the sequences
+    share a few pages (one prefix), and each must give what a batch of its own gives."""
+    lens = [(7 * b) % 41 for b in range(B)]
+    g = torch.Generator().manual_seed(B)
+    cache, _ = make(1, Hkv, d, dtype, fmt, [64])
+    table = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    x = rand(g, 2 * 41, Hkv, d, dtype=dtype).cuda()
+    skv.cache_append(x[:41], x[41:], cache, table[:1], i32([0]))
+    q = torch.randn(B, 1, G * Hkv, d, generator=g).to(dtype).cuda()
+    ws = torch.zeros(skv.paged_attn_workspace_bytes(B, 1, G * Hkv, Hkv, d, 1), dtype=torch.uint8, device="cuda")
+    out, lse = skv.paged_attn(q, cache, table, i32(lens), workspace=ws)
+    ok(ws)
+    for b in list(range(0, B, 37)) + [B - 1]:
+        ref.check_attention(out[b], lse[b], reference(q, cache, table, lens, b), dtype, fmt, f"sequence {b}")
+    # the rest against the same rows in plain torch, all at once
+    (k, v), _ = ref.read_rows(cache, [0], 0, 41)
+    k, v = (torch.from_numpy(t).cuda().permute(1, 0, 2) for t in (k, v))
+    s = torch.einsum("bhgd,htd->bhgt", q.double().view(B, Hkv, G, d), k) / math.sqrt(d)
+    s = s.masked_fill(torch.arange(41, device="cuda") >= i32(lens)[:, None, None, None], -math.inf)
+    # the bounds of cache_reference.attention_bounds, row by row (the 2^-25 of tiny weights goes into 2^-16)
+    size = torch.einsum("bhgd,htd->bhgt", q.double().view(B, Hkv, G, d).abs(), k.abs()).amax(-1) / math.sqrt(d)
+    dlogit = (2.0 ** -24 * (d + 12) * size + 2.0 ** -21).reshape(B, 1, -1)
+    want = torch.logsumexp(s, -1).view(B, 1, -1)
+    fin = want > -math.inf
+    assert torch.equal(lse > -math.inf, fin)
+    assert torch.all(((lse.double() - want).abs() <= dlogit + 2.0 ** -20 + 2.0 ** -22 * want.abs())[fin])
+    p = torch.nan_to_num(torch.softmax(s, -1))
+    o = torch.einsum("bhgt,htd->bhgd", p, v).reshape(B, 1, -1, d)
+    mass = torch.einsum("bhgt,htd->bhgd", p, v.abs()).reshape(B, 1, -1, d)
+    weight = 0.0 if dtype == F32 else 2.0 ** -11 if fmt == "e4m3" else 2.0 ** -8
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    assert torch.all((out.double() - o).abs() <= mass * (weight + 2.0 ** -15 + 2 * dlogit[..., None]) * (1 + half) + half * o.abs() + 1e-30)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "raw"])
 def test_attention_peaked_and_unequal_scales(fmt):
     """One key far above the others, values of very unequal size, equal keys: the running maximum and the value
@@ -368,6 +405,32 @@ def test_attention_device_errors_are_reported():
     assert not out[0].any() and torch.all(lse[0] == -math.inf)
     ref.check_attention(out[1], lse[1], reference(q, cache, table, lens, 1), BF, "e4m3")
     ok(ws)
+
+
+def test_host_values_are_checked():
+    cache, table, _ = filled(1, 1, 64, BF, "raw", [9])
+    q = torch.zeros(1, 1, 1, 64, dtype=BF, device="cuda")
+    for kw in (dict(window=-1), dict(window=(1 << 32) + 1), dict(scale=0.0)):
+        with pytest.raises(ValueError):
+            skv.paged_attn(q, cache, table, i32([9]), **kw)
+    for first, T in (([0], [-1]), ([-1], [1]), ([0], [(1 << 32) + 3]), ([1 << 33], [1]), ([0, 0], [1])):
+        with pytest.raises(ValueError):
+            skv.cache_read(cache, table, first, T)
+    with pytest.raises(skv.SkvError):
+        skv.cache_read(cache, table, [0], [65])
+    k, _ = skv.cache_read(cache, table, np.array([1]), np.array([3]))
+    assert k.shape == (3, 64)
+    bad = torch.zeros(2, 1, 64, dtype=BF, device="cuda")
+    for args in ((bad[:, :, :32], bad[:, :, :32]), (bad, bad[:1]), (bad.float(), bad.float()), (bad.transpose(0, 2), bad.transpose(0, 2))):
+        with pytest.raises(ValueError):
+            skv.cache_append(*args, cache, table, i32([9]))
+    with pytest.raises(ValueError):
+        skv.cache_append(bad, bad, cache, table, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        skv.cache_append(bad, bad, cache, table.long(), i32([9]))
+    with pytest.raises(skv.SkvError):   # rows that do not start on 16 bytes
+        x = torch.zeros(2, 2, 68, dtype=BF, device="cuda")[:, :1, 2:66]
+        skv.cache_append(x, x, cache, table, i32([9]))
 
 
 def test_strided_queries_other_stream_and_shared_workspace():
