@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                     if (d0 == 0) a.part_l[to] = sm.part[r];
                 }
             }
-            __syncthreads();
+            if (8 * (nt + TURN) < rows) __syncthreads();   // the last turn: the next piece's query rows bring a barrier
         }
         if (pc.np > 1) paged_finish_piece<__nv_bfloat16, D, ROWS, THREADS>(a, pc, sm.sched, sm.o);
         at = after;
@@ -591,11 +591,11 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
 // ---------------------------------------------------------------------------
 // fp32 queries: CUDA cores
 // ---------------------------------------------------------------------------
-// k_paged_f32: exact fp32 products on packed FMAs, out of the same rings. For the logits a lane takes tokens
-// n, n + 8 and rows r, r + 4 over all of d (16 FMAs to four 16-byte loads, both operands shared by neighbouring
-// lanes); for the outputs it takes d / 32 dimensions of all 8 rows (one load of its values per token and the
-// 8 weights broadcast). HBM bounds raw caches at d = 128: 16 KB per group are 712 clocks of one SM, the
-// group's ~1,400 instructions 350.
+// k_paged_f32: exact fp32 products on packed FMAs, out of the same rings. For the logits a lane takes four tokens x
+// four rows over a quarter of d (64 FMAs to eight 16-byte loads), and four lanes add their quarters up, each
+// keeping one token; for the outputs it takes d / 32 dimensions of all 8 rows (one load of its values per
+// token and the 8 weights broadcast). Raw caches at d = 128 are 16 KB per group, 712 clocks of one SM at the copy
+// rate; its ~350 shared-memory wavefronts and ~1,700 issue slots of one scheduler lie below that.
 constexpr int kF32Rows = 8;
 
 template <bool E4M3, int D, int W, int S>
@@ -630,7 +630,9 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
     constexpr int NR = kF32Rows, PER = D / 32, THREADS = 32 * W;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Sm &sm = *reinterpret_cast<Sm *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tq = lane & 7, rg = lane >> 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int part = lane & 3, tg = lane >> 2 & 3, rg = lane >> 4;   // quarter of d, tokens tg + 4 k, rows 4 rg + r
+    const int mine = tg + 4 * part;                                   // the token whose logits this lane ends up with
     GroupRing<W, S, 1, G::kGroup, Sm::kStage> ring;
     ring.init(sm.ring[warp][0], sm.full[warp]);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -671,7 +673,9 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
         __syncthreads();
         const int lo = pc.lo, hi = pc.hi, g0 = lo / kGroupTokens;
         const int g_end = hi > lo ? min((hi + kGroupTokens - 1) / kGroupTokens, g0 + pc.r1 * W) : 0;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float m[4], l[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.f;
         uint64_t o[PER][NR / 2];   // row pairs
 #pragma unroll
         for (int i = 0; i < PER; ++i)
@@ -683,76 +687,83 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
             if (!ring.skipped()) {
                 const uint8_t *buf = ring.data();
                 const int t0 = gi * kGroupTokens;
-                // ---- logits: tokens tq, tq + 8 x rows rg, rg + 4
-                uint64_t acc[2][2] = {};
-                const uint8_t *key = buf + tq * G::kVec;
-#pragma unroll 8
-                for (int c = 0; c < G::kChunks; ++c) {
-                    float x[2][CV::N];
+                // ---- logits: this quarter's share, then the sum of the quarters
+                uint64_t acc[4][4] = {};
+#pragma unroll 2
+                for (int i = 0; i < G::kChunks / 4; ++i) {
+                    const int c = 4 * i + part;
+                    float x[4][CV::N];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        CV::get(*reinterpret_cast<const uint4 *>(key + 8 * t * G::kVec + 16 * cache_chunk(c, tq, G::kChunks)), x[t]);
+                    for (int k = 0; k < 4; ++k) {
+                        const int n = tg + 4 * k;
+                        CV::get(*reinterpret_cast<const uint4 *>(buf + n * G::kVec + 16 * cache_chunk(c, n, G::kChunks)), x[k]);
+                    }
 #pragma unroll
-                    for (int i = 0; i < CV::N; i += 4)
+                    for (int e = 0; e < CV::N; e += 4)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float4 y = load4(&sm.q[rg + 4 * r][c * CV::N + i]);
+                        for (int r = 0; r < 4; ++r) {
+                            const float4 y = load4(&sm.q[4 * rg + r][c * CV::N + e]);
 #pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                acc[t][r] = ffma2(f2pack(x[t][i], x[t][i + 1]), f2pack(y.x, y.y), acc[t][r]);
-                                acc[t][r] = ffma2(f2pack(x[t][i + 2], x[t][i + 3]), f2pack(y.z, y.w), acc[t][r]);
+                            for (int k = 0; k < 4; ++k) {
+                                acc[k][r] = ffma2(f2pack(x[k][e], x[k][e + 1]), f2pack(y.x, y.y), acc[k][r]);
+                                acc[k][r] = ffma2(f2pack(x[k][e + 2], x[k][e + 3]), f2pack(y.z, y.w), acc[k][r]);
                             }
                         }
                 }
-                float s[2][2], vs[2] = {1.f, 1.f};
+                float s[4], vs = 1.f, ks = a.scale;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int n = tq + 8 * t;
-                    float ks = a.scale;
-                    if constexpr (E4M3) {
-                        ks *= scale_of(buf[2 * G::kBlock + n]);
-                        vs[t] = scale_of(buf[2 * G::kBlock + kGroupTokens + n]);
-                    }
-                    const bool in = t0 + n >= lo && t0 + n < hi;
-                    const float gap = static_cast<float>(hi - 1 - t0 - n);
+                for (int r = 0; r < 4; ++r) {
+                    float z[4];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
+                    for (int k = 0; k < 4; ++k) {
                         float x, y;
-                        f2unpack(acc[t][r], x, y);
-                        float z = (x + y) * ks;
-                        if (a.softcap > 0.f) z = capped_exact(z / a.softcap, a.softcap);
-                        s[t][r] = in ? (z - sm.slope[rg + 4 * r] * gap) * kLog2e : -INFINITY;
+                        f2unpack(acc[k][r], x, y);
+                        z[k] = x + y;
                     }
+                    // lane pairs swap tokens: the odd quarter keeps k = 1, 3, then the upper ones k = 2, 3
+                    const bool odd = part & 1, upper = part & 2;
+                    const float g0 = __shfl_xor_sync(0xffffffffu, odd ? z[0] : z[1], 1);
+                    const float g1 = __shfl_xor_sync(0xffffffffu, odd ? z[2] : z[3], 1);
+                    const float h0 = (odd ? z[1] : z[0]) + g0, h1 = (odd ? z[3] : z[2]) + g1;
+                    s[r] = (upper ? h1 : h0) + __shfl_xor_sync(0xffffffffu, upper ? h0 : h1, 2);
                 }
+                if constexpr (E4M3) {
+                    ks *= scale_of(buf[2 * G::kBlock + mine]);
+                    vs = scale_of(buf[2 * G::kBlock + kGroupTokens + mine]);
+                }
+                const bool in = t0 + mine >= lo && t0 + mine < hi;
+                const float gap = static_cast<float>(hi - 1 - t0 - mine);
                 // ---- running maximum and sum (each lane keeps the sum of its own tokens)
                 bool moved = false;
+                float p[4], f[4];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float top = fmaxf(s[0][r], s[1][r]);
+                for (int r = 0; r < 4; ++r) {
+                    float z = s[r] * ks;
+                    if (a.softcap > 0.f) z = capped_exact(z / a.softcap, a.softcap);
+                    z = in ? (z - sm.slope[4 * rg + r] * gap) * kLog2e : -INFINITY;
+                    float top = z;
 #pragma unroll
-                    for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    for (int x = 1; x < 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
                     top = fmaxf(top, m[r]);
                     const float ref = top > -INFINITY ? top : 0.f;   // no key yet: weights 2^-inf = 0
-                    const float f = ex2(m[r] - ref);
-                    moved |= f != 1.f;
+                    f[r] = ex2(m[r] - ref);
+                    moved |= f[r] != 1.f;
                     m[r] = top;
-                    l[r] *= f;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const float p = ex2(s[t][r] - ref);
-                        l[r] += p;
-                        sm.p[warp][tq + 8 * t][rg + 4 * r] = p * vs[t];
-                    }
-                    if (tq == 0) sm.f[warp][rg + 4 * r] = f;
+                    const float w = ex2(z - ref);
+                    l[r] = fmaf(l[r], f[r], w);
+                    p[r] = w * vs;
                 }
+                // a masked token's scale may be anything: its weight is never read
+                store4(&sm.p[warp][mine][4 * rg], make_float4(p[0], p[1], p[2], p[3]));
+                if ((lane & 15) == 0) store4(&sm.f[warp][4 * rg], make_float4(f[0], f[1], f[2], f[3]));
                 moved = __any_sync(0xffffffffu, moved);
                 __syncwarp();
                 if (moved) {
-                    const uint64_t *f = reinterpret_cast<const uint64_t *>(sm.f[warp]);
+                    const uint64_t *by = reinterpret_cast<const uint64_t *>(sm.f[warp]);
 #pragma unroll
                     for (int r = 0; r < NR / 2; ++r)
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) o[i][r] = mul2(o[i][r], f[r]);
+                        for (int i = 0; i < PER; ++i) o[i][r] = mul2(o[i][r], by[r]);
                 }
                 // ---- outputs: dimensions lane PER .. of the tokens that are seen (others may hold anything)
                 const int n0 = max(lo - t0, 0), n1 = min(hi - t0, kGroupTokens);
@@ -762,11 +773,13 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
                     const uint8_t *vp = buf + G::kBlock + n * G::kVec + 16 * cache_chunk(lane * bytes / 16, n, G::kChunks) + lane * bytes % 16;
                     float x[PER];
                     if constexpr (E4M3) {
-                        const float2 f0 = f16x2_to_f32(e4m3x2_to_f16x2(*reinterpret_cast<const unsigned short *>(vp)));
-                        x[0] = f0.x, x[1] = f0.y;
                         if constexpr (PER == 4) {
-                            const float2 f1 = f16x2_to_f32(e4m3x2_to_f16x2(*reinterpret_cast<const unsigned short *>(vp + 2)));
-                            x[2] = f1.x, x[3] = f1.y;
+                            const uint32_t u = *reinterpret_cast<const uint32_t *>(vp);
+                            const float2 f0 = f16x2_to_f32(cvt_lo(u)), f1 = f16x2_to_f32(cvt_hi(u));
+                            x[0] = f0.x, x[1] = f0.y, x[2] = f1.x, x[3] = f1.y;
+                        } else {
+                            const float2 f0 = f16x2_to_f32(e4m3x2_to_f16x2(*reinterpret_cast<const unsigned short *>(vp)));
+                            x[0] = f0.x, x[1] = f0.y;
                         }
                     } else if constexpr (PER == 4) {
                         const float4 u = *reinterpret_cast<const float4 *>(vp);
@@ -792,11 +805,11 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
         // ---- join the warps; those that had no group have nothing to add
         const int act = max(1, min(W, g_end - (g0 + pc.r0 * W)));
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < 4; ++r) {
             float sum = l[r];
 #pragma unroll
-            for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            if (tq == 0) sm.m[warp][rg + 4 * r] = m[r], sm.l[warp][rg + 4 * r] = sum;
+            for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            if ((lane & 15) == 0) sm.m[warp][4 * rg + r] = m[r], sm.l[warp][4 * rg + r] = sum;
         }
 #pragma unroll
         for (int r = 0; r < NR / 2; ++r)
@@ -841,7 +854,7 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
                 if (d0 == 0) a.part_l[to] = sm.part[r];
             }
         }
-        __syncthreads();
+        // no barrier: what follows writes none of this before the next one (the next piece's query rows')
         if (pc.np > 1) paged_finish_piece<float, D, NR, THREADS>(a, pc, sm.sched, sm.o);
         at = paged_next(sm.sched, at + 1);
     }
