@@ -279,12 +279,21 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedPiece 
     const int rows = min(PASS, a.rows - row0);
     const auto slot = [&](int k, int row) { return (2 * static_cast<int64_t>(c0 + k) + (k == 0 ? 1 : 0)) * PASS + row; };
     float *parts = scratch + rows * np;   // the rows' log2 partitions
-#pragma unroll 1
-    for (int row = threadIdx.x >> 5; row < rows; row += THREADS / 32) {
+    constexpr int WARPS = THREADS / 32, RPW = (PASS + WARPS - 1) / WARPS;   // rows per warp, loaded together
+    const int warp = threadIdx.x >> 5;
+    float first[RPW];
+#pragma unroll
+    for (int i = 0; i < RPW; ++i)
+        first[i] = warp + i * WARPS < rows && lane < np ? __ldcg(a.part_l + slot(lane, warp + i * WARPS)) : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+        const int row = warp + i * WARPS;
+        if (row >= rows) break;
         float *wt = scratch + row * np;
-        float top = -INFINITY, sum = 0.f;
+        float top = first[i], sum = 0.f;
+        if (lane < np) wt[lane] = first[i];
 #pragma unroll 1
-        for (int k = lane; k < np; k += 32) {
+        for (int k = lane + 32; k < np; k += 32) {
             wt[k] = __ldcg(a.part_l + slot(k, row));
             top = fmaxf(top, wt[k]);
         }
