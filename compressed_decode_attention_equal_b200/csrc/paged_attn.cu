@@ -36,11 +36,9 @@ struct MmaSmem {
     using G = CacheGeom<__nv_bfloat16, E4M3, D>;
     static constexpr int kStage = (TP * G::kGroup + 127) / 128 * 128;
     static constexpr int kRows = 8 * NT;
-    // rounds that a unit's query load and outputs take as long as: 1, 2, 3, 4 measured 90.0, 74.9, 76.8, 80.0 us
-    // (64 ragged sequences x 16 heads, one row each), and 2, 3, 4 with 28 rows 48.4, 49.5, 47.1 us (48 x 4 heads)
+    // rounds that a unit's query load and outputs take as long as: 1, 2, 3 measured 88.1, 73.5, 75.4 us with one row
+    // (64 ragged sequences x 16 heads), and 1, 2, 3, 4 with 28 rows 56.5, 47.3, 48.2, 46.8 us (48 x 4 heads)
     static constexpr int kCost = NT == 1 ? 2 : 4;
-    // least weight per CTA: one sequence of 10,500 tokens and 2 heads 14.3 us at 2, 15.5 us at 4
-    static constexpr int kLeast = 2;
     static constexpr int kQRow = 2 * D + 8;      // bytes of a query row: 8 more than 2 D against bank conflicts
     static constexpr int kMerge = 33;            // words per accumulator element of a warp's 32 lanes
     static constexpr int kMaxCtas = CTAS * 160;  // the join of a unit's pieces keeps a word per row and piece in o
@@ -218,6 +216,9 @@ struct GroupRing {
 //   Weights are rounded to the matrix type (fp16 2^-11, bf16 2^-8 relative): the second product runs on
 //   16-bit operands, and the partition keeps the fp32 weights. Sums and maxima are fp32. The reference maximum
 //   moves only when a logit exceeds it by 2^8, so that the rescale of O runs rarely.
+// Measured: 32 sequences x 4 heads x 32,768 e4m3 keys at 7 rows take 172 us, 97% of the copy rate (raw, ragged:
+// 79.5 us, 94%). An mma.sync, a conversion and an FMA add up on one scheduler here instead of overlapping, so
+// that many rows are bound by the instruction rate: 28 rows over 8 x 4 x 16,384 e4m3 keys take 61 us, 34%.
 template <bool E4M3, int D, int NT, int W, int S, int CTAS, int TP>
 __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
     using Sm = MmaSmem<E4M3, D, NT, W, S, CTAS, TP>;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     paged_schedule<THREADS, W, TT, Sm::kCost>(a, sm.sched);
-    paged_pieces<W, TT, Sm::kCost, Sm::kLeast>(a, sm.sched, 0);
+    paged_pieces<W, TT, Sm::kCost>(a, sm.sched, 0);
 
     constexpr int PER = D / 32, RPW = (ROWS + W - 1) / W;   // query elements per lane and row, rows per warp
     uint32_t qx[RPW][PER / 2];
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
             if (at < kPieceTable) break;
             __syncthreads();
             from += kPieceTable;
-            paged_pieces<W, TT, Sm::kCost, Sm::kLeast>(a, sm.sched, from);
+            paged_pieces<W, TT, Sm::kCost>(a, sm.sched, from);
             at = paged_next(sm.sched, 0);
             fresh = true;
             continue;
@@ -595,7 +596,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
 // four rows over a quarter of d (64 FMAs to eight 16-byte loads), and four lanes add their quarters up, each
 // keeping one token; for the outputs it takes d / 32 dimensions of all 8 rows (one load of its values per
 // token and the 8 weights broadcast). Raw caches at d = 128 are 16 KB per group, 712 clocks of one SM at the copy
-// rate; its ~350 shared-memory wavefronts and ~1,700 issue slots of one scheduler lie below that.
+// rate; its ~350 shared-memory wavefronts and ~1,700 issue slots of one scheduler lie below that, but
+// 8 warps do not hide a group's latency: 8 sequences x 4 heads x 8,192 keys take 64 us, 65% of the copy rate
+// (88 us with two tokens x two rows per lane).
 constexpr int kF32Rows = 8;
 
 template <bool E4M3, int D, int W, int S>
@@ -603,7 +606,7 @@ struct F32Smem {
     using G = CacheGeom<float, E4M3, D>;
     static constexpr int kStage = (G::kGroup + 127) / 128 * 128;
     static constexpr int kMaxCtas = 160;             // the join of a unit's pieces keeps a word per row and piece in o
-    static constexpr int kCost = 2, kLeast = 2;
+    static constexpr int kCost = 2;
     static constexpr int kOut = W * kF32Rows * D, kJoin = kF32Rows * (kMaxCtas + 1);
     alignas(128) uint8_t ring[W][S][kStage];
     alignas(16) float o[kOut > kJoin ? kOut : kJoin];   // [W][rows][D]
@@ -638,7 +641,7 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     paged_schedule<THREADS, W, kGroupTokens, Sm::kCost>(a, sm.sched);
-    paged_pieces<W, kGroupTokens, Sm::kCost, Sm::kLeast>(a, sm.sched, 0);
+    paged_pieces<W, kGroupTokens, Sm::kCost>(a, sm.sched, 0);
     int from = 0, at = paged_next(sm.sched, 0);
     bool fresh = true;   // a new table: nothing is ahead
 #pragma unroll 1
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
             if (at < kPieceTable) break;
             __syncthreads();
             from += kPieceTable;
-            paged_pieces<W, kGroupTokens, Sm::kCost, Sm::kLeast>(a, sm.sched, from);
+            paged_pieces<W, kGroupTokens, Sm::kCost>(a, sm.sched, from);
             at = paged_next(sm.sched, 0);
             fresh = true;
             continue;
@@ -928,6 +931,10 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     // at d = 64 two groups make a tile, which halves what a tile costs beside its products: 32 x 8 heads x 8,192 keys
     // 70.9 -> 61.9 us (e4m3), 93.9 -> 86.7 us (raw)
     constexpr int TP = D == 64 ? 2 : 1;
+    // Warps and CTAs per SM. e4m3, 8 rows: two CTAs of 8 warps at 128 registers (7B batch 172 us; one CTA of 8 warps
+    // 219 us: too few to hide a tile's latency). Raw tiles are twice the bytes for the same work: one CTA of 8
+    // warps (79.3 us; two of 4 84.7). More rows need the registers: 16 and 28 rows 45.0 and 61.0 us; with three
+    // and two CTAs of 4 warps 48.2 and 69.3.
     if constexpr (E4M3) {
         if (a.pass_rows == 8) return launch_mma<E4M3, D, 1, 8, 2, 2, TP>(a, s);
         if (a.pass_rows == 16) return launch_mma<E4M3, D, 2, 8, 3, 1, TP>(a, s);

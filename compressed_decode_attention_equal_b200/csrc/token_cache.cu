@@ -16,7 +16,7 @@ namespace {
 // append: a warp takes kHeads heads of some consecutive tokens, half of it the keys and half the values,
 // d / 16 elements per lane; the next token's loads are in flight while one is quantised, and the lanes
 // look the tokens' pages up side by side. The instruction rate bounds it for long prompts (74,211 tokens x 4
-// heads: 40.9 us, 86% of the copy rate, 48.0 us without the limit of 64 registers): one round
+// heads of bf16 to e4m3: 41.3 us, 85% of the copy rate; 48 us without the limit of 64 registers): one round
 // of page lookups per warp, bf16 maxima of two vectors in one word and packed products keep it there.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
@@ -426,8 +426,9 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t
 template <typename T, bool E4M3, int D>
 cudaError_t append_d(const AppendArgs &a0, cudaStream_t s) {
     AppendArgs a = a0;
-    // Flat rows where a step of whole tokens would be partly empty: 74,211 tokens x 1 head 56.8 -> FLATNEW us; they cost
-    // two more shuffles and products per row (x 4 heads 40.9 -> FLATOLD us), so that other head counts do without.
+    // Flat rows where a step of whole tokens would be partly empty: 74,211 tokens x 1 head take 32.8 us instead of
+    // 56.8. They cost shuffles and address products per row (x 4 heads 60.1 us instead of 41.3), so that other head
+    // counts do without.
     const bool flat = a.Hkv % kHeads != 0;
     const int64_t all = flat ? (static_cast<int64_t>(a.n_tokens) * a.Hkv + kHeads - 1) / kHeads : static_cast<int64_t>(a.n_tokens) * (a.Hkv / kHeads);
     // steps of a warp: one while there are not enough warps for the GPU
