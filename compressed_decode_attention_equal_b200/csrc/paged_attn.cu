@@ -14,12 +14,8 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// cap tanh(t) with tanh t = 1 - 2 / (e^(2t) + 1), whose absolute error stays within a few ulps of 1 over the
-// whole range (the hardware tanh's 2^-11 would show in the logits): with a true division for fp32 results,
-// with the approximate exponential and reciprocal (2^-22 and 2^-23 relative) in front of 16-bit products.
-__device__ __forceinline__ float capped_exact(float t, float cap) {
-    return cap * (1.0f - 2.0f / (exp2f(t * (2.0f * kLog2e)) + 1.0f));
-}
+// cap tanh(t) in front of 16-bit products: tanh t = 1 - 2 / (e^(2t) + 1), whose absolute error stays within a few
+// ulps of 1 over the whole range (the hardware tanh's 2^-11 would show in the logits)
 __device__ __forceinline__ float capped(float t, float cap) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(t * (2.0f * kLog2e)) + 1.0f));
@@ -742,17 +738,17 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     float z = s[r] * ks;
-                    if (a.softcap > 0.f) z = capped_exact(z / a.softcap, a.softcap);
-                    z = in ? (z - sm.slope[4 * rg + r] * gap) * kLog2e : -INFINITY;
+                    if (a.softcap > 0.f) z = a.softcap * tanhf(z / a.softcap);
+                    z = in ? z - sm.slope[4 * rg + r] * gap : -INFINITY;
                     float top = z;
 #pragma unroll
                     for (int x = 1; x < 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
                     top = fmaxf(top, m[r]);
                     const float ref = top > -INFINITY ? top : 0.f;   // no key yet: weights 2^-inf = 0
-                    f[r] = ex2(m[r] - ref);
+                    f[r] = ex2((m[r] - ref) * kLog2e);   // differences first: a base-2 logit would be rounded at its full size
                     moved |= f[r] != 1.f;
                     m[r] = top;
-                    const float w = ex2(z - ref);
+                    const float w = ex2((z - ref) * kLog2e);
                     l[r] = fmaf(l[r], f[r], w);
                     p[r] = w * vs;
                 }
@@ -832,12 +828,12 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
 #pragma unroll
             for (int x = 1; x < W; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             top = top > -INFINITY ? top : 0.f;
-            const float f = ex2(mine - top);
+            const float f = ex2((mine - top) * kLog2e);
             float sum = f * sm.l[w][r];
 #pragma unroll
             for (int x = 1; x < W; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
             sm.m[w][r] = sum == 0.f ? 0.f : f * __frcp_rn(sum);
-            if (w == 0) sm.part[r] = sum == 0.f ? -INFINITY : top + __log2f(sum);
+            if (w == 0) sm.part[r] = sum == 0.f ? -INFINITY : fmaf(top, kLog2e, __log2f(sum));
         }
         __syncthreads();
         for (int i = tid; i < rows * (D / 4); i += THREADS) {
