@@ -32,8 +32,10 @@ skv_status check_cache(int dtype, int format, int B, int Hkv, int d, int max_pag
     return SKV_OK;
 }
 
-bool pool_ok(const skv_token_cache *c) {
-    return c && c->pages && aligned(c->pages, 16) && c->num_pages >= 0 && c->num_pages <= INT32_MAX;
+// Groups are counted in 32 bits (2^31 of the smallest, 2,080 bytes, are 4 TB).
+skv_status check_pool(const skv_token_cache *c, int Hkv) {
+    if (!c || !c->pages || !aligned(c->pages, 16) || c->num_pages < 0) return SKV_ERR_INVALID_ARG;
+    return c->num_pages > INT32_MAX / (static_cast<int64_t>(Hkv) * kPageGroups) ? SKV_ERR_UNSUPPORTED : SKV_OK;
 }
 
 // Vectors are read 16 bytes at a time. A dimension of one element has no stride that matters.
@@ -85,10 +87,11 @@ skv_status skv_cache_append(const void *k, const void *v, skv_dtype dtype, int64
                             int n_tokens, const int32_t *cu_new, skv_cache_format format, const skv_token_cache *cache,
                             const int32_t *page_table, int max_pages, const int32_t *lens, int32_t *new_lens,
                             void *workspace, size_t ws_bytes, void *stream) {
-    const skv_status st = check_cache(dtype, format, B, Hkv, d, max_pages);
+    skv_status st = check_cache(dtype, format, B, Hkv, d, max_pages);
     if (st != SKV_OK) return st;
     if (n_tokens < 0 || (!cu_new && n_tokens % B != 0)) return SKV_ERR_INVALID_ARG;
-    if ((n_tokens > 0 && (!k || !v)) || !page_table || !lens || !new_lens || !pool_ok(cache)) return SKV_ERR_INVALID_ARG;
+    if ((n_tokens > 0 && (!k || !v)) || !page_table || !lens || !new_lens) return SKV_ERR_INVALID_ARG;
+    if ((st = check_pool(cache, Hkv)) != SKV_OK) return st;
     const int64_t elem = dtype == SKV_BF16 ? 2 : 4;
     if (!stride_ok(k_token_stride, n_tokens, elem) || !stride_ok(k_head_stride, Hkv, elem) ||
         !stride_ok(v_token_stride, n_tokens, elem) || !stride_ok(v_head_stride, Hkv, elem))
@@ -128,9 +131,10 @@ skv_status skv_cache_append(const void *k, const void *v, skv_dtype dtype, int64
 skv_status skv_cache_read(const skv_token_cache *cache, skv_dtype dtype, skv_cache_format format, int B, int Hkv, int d,
                           const int32_t *first_host, const int32_t *T_host, const int32_t *page_table, int max_pages,
                           void *k, void *v, void *workspace, size_t ws_bytes, void *stream) {
-    const skv_status st = check_cache(dtype, format, B, Hkv, d, max_pages);
+    skv_status st = check_cache(dtype, format, B, Hkv, d, max_pages);
     if (st != SKV_OK) return st;
-    if (!first_host || !T_host || !page_table || !aligned(page_table, 4) || !pool_ok(cache)) return SKV_ERR_INVALID_ARG;
+    if (!first_host || !T_host || !page_table || !aligned(page_table, 4)) return SKV_ERR_INVALID_ARG;
+    if ((st = check_pool(cache, Hkv)) != SKV_OK) return st;
     ReadTable t;
     int64_t rows = 0, items = 0;
     for (int b = 0; b < B; ++b) {
@@ -178,9 +182,10 @@ skv_status skv_paged_attn(const void *q, skv_dtype dtype, int64_t q_seq_stride, 
     PagedArgs a{};
     size_t total = 0;
     if (format != SKV_CACHE_RAW && format != SKV_CACHE_E4M3) return SKV_ERR_INVALID_ARG;
-    const skv_status st = plan_paged(dtype, B, R, Hq, Hkv, d, max_pages, &a, &total);
+    skv_status st = plan_paged(dtype, B, R, Hq, Hkv, d, max_pages, &a, &total);
     if (st != SKV_OK) return st;
-    if (!q || !page_table || !lens || !out || !lse || !pool_ok(cache)) return SKV_ERR_INVALID_ARG;
+    if (!q || !page_table || !lens || !out || !lse) return SKV_ERR_INVALID_ARG;
+    if ((st = check_pool(cache, Hkv)) != SKV_OK) return st;
     const int64_t elem = dtype == SKV_BF16 ? 2 : 4;
     if (!stride_ok(q_seq_stride, B, elem) || !stride_ok(q_row_stride, R, elem) || !stride_ok(q_head_stride, Hq, elem))
         return SKV_ERR_INVALID_ARG;

@@ -13,15 +13,16 @@ namespace skv {
 namespace {
 
 // ---------------------------------------------------------------------------
-// append: a warp takes kHeads heads of some consecutive tokens, half of it the keys and half the values,
-// d / 16 elements per lane; the next token's loads are in flight while one is quantised, and the lanes
-// look the tokens' pages up side by side. The instruction rate bounds it for long prompts (74,211 tokens x 4
-// heads of bf16 to e4m3: 41.3 us, 85% of the copy rate; 48 us without the limit of 64 registers): one round
-// of page lookups per warp, bf16 maxima of two vectors in one word and packed products keep it there.
+// append: a vector is 8 elements per lane, so that a warp takes the key and value of one row (d = 128) or two
+// (d = 64) at once, kHeads times that per step; the next step's loads are in flight while one is quantised, and
+// the lanes look the tokens' pages up side by side. The instruction rate bounds it for long prompts (74,211 tokens
+// x 4 heads of bf16 to e4m3: 40.1 us, 88% of the copy rate; without the limit of 64 registers 48): one round of
+// page lookups per warp, bf16 maxima of two vectors in one word and packed products keep it there.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 constexpr int kHeads = 4;          // independent loads in flight per lane
-constexpr int kAppendTokens = 4;   // most tokens of a warp: 2, 4, 8, 16 measured 51.5, 43.7, 45.8, 53.3 us (74,211 tokens x 4 heads)
+constexpr int kLaneElems = 8;
+constexpr int kAppendTokens = 4;   // most steps of a warp: 2, 4, 8, 16 measured 51.5, 43.7, 45.8, 53.3 us (74,211 tokens x 4 heads)
 
 // two fp32 to two e4m3 codes (round to nearest even, saturating; lo in the low byte)
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
@@ -38,18 +39,12 @@ __device__ __forceinline__ int scale_exponent(float a) {
     return a > 0.f ? min(max(e, kScaleExpMin), kScaleExpMax) : 0;
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void load_row(const T *p, uint32_t (&w)[N * sizeof(T) / 4]) {
-    constexpr int W = N * sizeof(T) / 4;   // 2, 4 or 8 words, 8- or 16-byte aligned
-    if constexpr (W == 2) {
-        const uint2 u = *(reinterpret_cast<const uint2 *>(p));
-        w[0] = u.x, w[1] = u.y;
-    } else {
+template <typename T, int W>
+__device__ __forceinline__ void load_row(const T *p, uint32_t (&w)[W]) {   // 4 or 8 words, 16-byte aligned
 #pragma unroll
-        for (int i = 0; i < W; i += 4) {
-            const uint4 u = *(reinterpret_cast<const uint4 *>(p) + i / 4);
-            w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
-        }
+    for (int i = 0; i < W; i += 4) {
+        const uint4 u = *(reinterpret_cast<const uint4 *>(p) + i / 4);
+        w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
     }
 }
 
@@ -92,10 +87,10 @@ __device__ __forceinline__ uint32_t magnitude(const uint32_t (&w)[W], bool finit
     return top;
 }
 
-// Scale exponents of kHeads vectors, each spread over 16 lanes that agree on it; the whole warp takes part.
+// Scale exponents of kHeads vectors, each spread over LANES lanes that agree on it; the whole warp takes part.
 // bf16 magnitudes are reduced two vectors to a word. FINITE false: one over all elements, false if some vector
 // holds an infinity (a bf16 NaN is passed over, an fp32 one counts as an infinity).
-template <typename T, int W, bool FINITE>
+template <typename T, int W, int LANES, bool FINITE>
 __device__ __forceinline__ bool scale_exponents(const uint32_t (&w)[kHeads][W], int (&e)[kHeads]) {
     constexpr bool PAIRS = sizeof(T) == 2;
     constexpr int REGS = PAIRS ? kHeads / 2 : kHeads;
@@ -110,7 +105,7 @@ __device__ __forceinline__ bool scale_exponents(const uint32_t (&w)[kHeads][W], 
         }
     }
 #pragma unroll
-    for (int s = 8; s; s >>= 1)
+    for (int s = LANES / 2; s; s >>= 1)
 #pragma unroll
         for (int i = 0; i < REGS; ++i) {
             const uint32_t other = __shfl_xor_sync(0xffffffffu, r[i], s);
@@ -150,54 +145,65 @@ __device__ __forceinline__ void quantise(const uint32_t (&w)[W], int e, uint32_t
     }
 }
 
-// FLAT false: a step is kHeads heads of one token. FLAT true: kHeads consecutive (token, head) rows, whatever
-// their tokens; for head counts that kHeads does not divide, whose steps would be partly empty.
+// FLAT false: a step is that many heads of one token. FLAT true: as many consecutive (token, head) rows, whatever
+// their tokens; for head counts that do not fill steps (74,211 tokens x 1 head 26.0 us instead of 56.8; 4 heads
+// would take 44.6 instead of 40.1 with a lookup per row).
 template <typename T, bool E4M3, int D, bool FLAT>
 __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_cache_append(const AppendArgs a) {
     using G = CacheGeom<T, E4M3, D>;
-    constexpr int N = D / 16;                     // elements per lane
-    constexpr int W = N * static_cast<int>(sizeof(T)) / 4;
+    constexpr int N = kLaneElems, W = N * static_cast<int>(sizeof(T)) / 4;
+    constexpr int LANES = D / N, SUBS = 32 / (2 * LANES);   // lanes of a vector, rows side by side
+    constexpr int ROWS = kHeads * SUBS;                     // rows of a step
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+    const int lane = threadIdx.x & 31, sub = lane / (2 * LANES), half = lane / LANES & 1, l = lane % LANES;
     const unsigned item = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-    // this warp: tokens i0 .. i0 + count - 1, heads h0 .. h0 + kHeads - 1; or (FLAT) rows i0 .. i0 + count - 1
+    // this warp: tokens i0 .. i0 + count - 1, heads h0 .. h0 + ROWS - 1; or (FLAT) rows i0 .. i0 + count - 1.
+    // n_tokens * Hkv fits 32 bits (checked on the host); items may reach a little beyond, so 64 here.
     int64_t i0;
     int h0 = 0, count;
     if constexpr (FLAT) {
-        i0 = static_cast<int64_t>(item) * (a.per_warp * kHeads);
-        count = static_cast<int>(max(min(static_cast<int64_t>(a.per_warp * kHeads), static_cast<int64_t>(a.n_tokens) * a.Hkv - i0), int64_t{0}));
+        i0 = static_cast<int64_t>(item) * (a.per_warp * ROWS);
+        count = static_cast<int>(max(min(static_cast<int64_t>(a.per_warp * ROWS), static_cast<int64_t>(a.n_tokens) * a.Hkv - i0), int64_t{0}));
     } else {
-        const unsigned chunks = a.Hkv / kHeads, part = item / chunks;
-        h0 = static_cast<int>(item - part * chunks) * kHeads;
+        const unsigned chunks = a.Hkv / ROWS, part = item / chunks;
+        h0 = static_cast<int>(item - part * chunks) * ROWS;
         i0 = static_cast<int64_t>(part) * a.per_warp;
         count = static_cast<int>(max(min(static_cast<int64_t>(a.per_warp), a.n_tokens - i0), int64_t{0}));
     }
-    const int steps = FLAT ? (count + kHeads - 1) / kHeads : count;
-    // FLAT: lane r holds the token and head of row i0 + r
-    const int token = static_cast<int>(FLAT ? (i0 + lane) / a.Hkv : i0 + lane);
-    const int head = FLAT ? static_cast<int>(i0 + lane - static_cast<int64_t>(token) * a.Hkv) : h0;
-    const T *src = (half ? static_cast<const T *>(a.v) : static_cast<const T *>(a.k)) + l * N;
+    const int steps = FLAT ? (count + ROWS - 1) / ROWS : count;
     const int64_t token_stride = half ? a.v_token : a.k_token, head_stride = half ? a.v_head : a.k_head;
+    // where this lane loads next; FLAT walks over the rows i0 + sub, i0 + sub + SUBS, ...
+    const T *src = (half ? static_cast<const T *>(a.v) : static_cast<const T *>(a.k)) + l * N;
+    int hd = h0 + sub;
+    if constexpr (FLAT) {
+        const int64_t tk = (i0 + sub) / a.Hkv;
+        hd = static_cast<int>(i0 + sub - tk * a.Hkv);
+        src += tk * token_stride + hd * head_stride;
+    } else {
+        src += i0 * token_stride + hd * head_stride;
+    }
     const auto load_step = [&](int t, uint32_t (&w)[kHeads][W]) {
         if (t >= steps) return;
 #pragma unroll
         for (int j = 0; j < kHeads; ++j) {
             if constexpr (FLAT) {
-                const int r = t * kHeads + j;
-                const int64_t tk = __shfl_sync(0xffffffffu, token, r), hd = __shfl_sync(0xffffffffu, head, r);
-                if (r < count) load_row<T, N>(src + tk * token_stride + hd * head_stride, w[j]);
+                if (t * ROWS + j * SUBS + sub < count) load_row<T, W>(src, w[j]);
+                src += SUBS * head_stride;
+                for (hd += SUBS; hd >= a.Hkv; hd -= a.Hkv) src += token_stride - a.Hkv * head_stride;
             } else {
-                load_row<T, N>(src + (i0 + t) * token_stride + (h0 + j) * head_stride, w[j]);
+                load_row<T, W>(src + j * SUBS * head_stride, w[j]);
             }
         }
+        if constexpr (!FLAT) src += token_stride;
     };
     uint32_t next[kHeads][W] = {};
     load_step(0, next);
-    // lane t: where token (row) t goes (page -1: nowhere)
-    int where_page = -1, where_slot = 0;
+    // lane t: the group that token (row) t goes to (-1: none; the first head's) and its slot there
+    int where = -1, slot16 = 0;
     if (lane < count) {
-        const int i = token;
+        const int i = static_cast<int>(FLAT ? (i0 + lane) / a.Hkv : i0 + lane);
+        const int head = FLAT ? static_cast<int>(i0 + lane - static_cast<int64_t>(i) * a.Hkv) : h0;
         int b, off;
         bool ok = true;
         if (a.cu) {
@@ -220,12 +226,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_c
             const int len = a.lens[b];
             const int64_t pos = static_cast<int64_t>(len) + off;
             if (len >= 0 && pos < static_cast<int64_t>(a.max_pages) * SKV_CACHE_PAGE_TOKENS) {   // else flagged below
-                where_page = a.page_table[static_cast<int64_t>(b) * a.max_pages + pos / SKV_CACHE_PAGE_TOKENS];
-                where_slot = static_cast<int>(pos) % SKV_CACHE_PAGE_TOKENS;
-                if (where_page < 0 || where_page >= a.num_pages) {
-                    raise_flag(a.flags, FLAG_BAD_PAGE);
-                    where_page = -1;
-                }
+                const int page = a.page_table[static_cast<int64_t>(b) * a.max_pages + pos / SKV_CACHE_PAGE_TOKENS];
+                const int slot = static_cast<int>(pos) % SKV_CACHE_PAGE_TOKENS;
+                slot16 = slot % kGroupTokens;
+                if (page < 0 || page >= a.num_pages) raise_flag(a.flags, FLAG_BAD_PAGE);
+                else where = (page * a.Hkv + head) * kPageGroups + slot / kGroupTokens;   // fits: checked on the host
             }
         }
     }
@@ -265,49 +270,38 @@ __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_c
 #pragma unroll
             for (int q = 0; q < W; ++q) w[j][q] = next[j][q];
         load_step(t + 1, next);
-        int n = 0;
-        uint8_t *grp = nullptr;
+        int group = 0, n = 0;
         if constexpr (!FLAT) {
-            const int page = __shfl_sync(0xffffffffu, where_page, t), slot = __shfl_sync(0xffffffffu, where_slot, t);
-            if (page < 0) continue;
-            n = slot % kGroupTokens;
-            grp = a.pages + ((static_cast<int64_t>(page) * a.Hkv + h0) * kPageGroups + slot / kGroupTokens) * G::kGroup;
+            group = __shfl_sync(0xffffffffu, where, t);
+            if (group < 0) continue;
+            n = __shfl_sync(0xffffffffu, slot16, t);
         }
         int e[kHeads];
         if constexpr (E4M3)
-            if (!scale_exponents<T, W, false>(w, e)) scale_exponents<T, W, true>(w, e);
+            if (!scale_exponents<T, W, LANES, false>(w, e)) scale_exponents<T, W, LANES, true>(w, e);
+        uint8_t *grp = a.pages + (static_cast<int64_t>(group) + sub * kPageGroups) * G::kGroup;
 #pragma unroll
         for (int j = 0; j < kHeads; ++j) {
             if constexpr (FLAT) {
-                const int r = (t * kHeads + j) & 31;
-                const int page = __shfl_sync(0xffffffffu, where_page, r), slot = __shfl_sync(0xffffffffu, where_slot, r);
-                const int hd = __shfl_sync(0xffffffffu, head, r);
-                if (page < 0) continue;   // rows behind the last one among them
-                n = slot % kGroupTokens;
-                grp = a.pages + ((static_cast<int64_t>(page) * a.Hkv + hd) * kPageGroups + slot / kGroupTokens) * G::kGroup;
-            } else if (j > 0) {
-                grp += kPageGroups * G::kGroup;   // the next head
+                const int r = (t * ROWS + j * SUBS + sub) & 31;
+                group = __shfl_sync(0xffffffffu, where, r);
+                n = __shfl_sync(0xffffffffu, slot16, r);
+                if (group < 0) continue;   // rows behind the last one among them
+                grp = a.pages + static_cast<int64_t>(group) * G::kGroup;
             }
             uint8_t *row = grp + half * G::kBlock + n * G::kVec;
             uint8_t *exps = grp + 2 * G::kBlock + half * kGroupTokens + n;
+            if constexpr (!FLAT) grp += SUBS * kPageGroups * G::kGroup;   // the next heads
             if constexpr (E4M3) {
                 uint32_t c[N / 4];
                 quantise<T, N, W>(w[j], e[j], c);
-                uint8_t *to = row + 16 * cache_chunk(l * N / 16, n, G::kChunks) + l * N % 16;
-                if constexpr (N == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(c[0], c[1]);
-                else *reinterpret_cast<uint32_t *>(to) = c[0];
+                *reinterpret_cast<uint2 *>(row + 16 * cache_chunk(l * N / 16, n, G::kChunks) + l * N % 16) = make_uint2(c[0], c[1]);
                 if (l == 0) *exps = static_cast<uint8_t>(e[j] + 127);
             } else {
-                const int byte = l * W * 4;
-                if constexpr (W == 2) {
-                    *reinterpret_cast<uint2 *>(row + 16 * cache_chunk(byte / 16, n, G::kChunks) + byte % 16) =
-                        make_uint2(w[j][0], w[j][1]);
-                } else {
 #pragma unroll
-                    for (int q = 0; q < W; q += 4)
-                        *reinterpret_cast<uint4 *>(row + 16 * cache_chunk(byte / 16 + q / 4, n, G::kChunks)) =
-                            make_uint4(w[j][q], w[j][q + 1], w[j][q + 2], w[j][q + 3]);
-                }
+                for (int q = 0; q < W; q += 4)
+                    *reinterpret_cast<uint4 *>(row + 16 * cache_chunk((l * W + q) / 4, n, G::kChunks)) =
+                        make_uint4(w[j][q], w[j][q + 1], w[j][q + 2], w[j][q + 3]);
             }
         }
     }
@@ -426,16 +420,14 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t
 template <typename T, bool E4M3, int D>
 cudaError_t append_d(const AppendArgs &a0, cudaStream_t s) {
     AppendArgs a = a0;
-    // Flat rows where a step of whole tokens would be partly empty: 74,211 tokens x 1 head take 32.8 us instead of
-    // 56.8. They cost shuffles and address products per row (x 4 heads 60.1 us instead of 41.3), so that other head
-    // counts do without.
-    const bool flat = a.Hkv % kHeads != 0;
-    const int64_t all = flat ? (static_cast<int64_t>(a.n_tokens) * a.Hkv + kHeads - 1) / kHeads : static_cast<int64_t>(a.n_tokens) * (a.Hkv / kHeads);
+    constexpr int ROWS = kHeads * (128 / D);   // rows of a step
+    const bool flat = a.Hkv % ROWS != 0;
+    const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.Hkv, all = (rows + ROWS - 1) / ROWS;   // steps
     // steps of a warp: one while there are not enough warps for the GPU
     const int64_t per = all / (148 * 32);
     a.per_warp = static_cast<int>(per < 1 ? 1 : per > kAppendTokens ? kAppendTokens : per);
     const int64_t items = flat ? (all + a.per_warp - 1) / a.per_warp
-                               : (a.n_tokens + a.per_warp - 1) / a.per_warp * static_cast<int64_t>(a.Hkv / kHeads);
+                               : (a.n_tokens + a.per_warp - 1) / a.per_warp * static_cast<int64_t>(a.Hkv / ROWS);
     const int64_t grid = items > 0 ? (items + kAppendWarps - 1) / kAppendWarps : 1;   // the lengths are written at least
     return flat ? launch(k_cache_append<T, E4M3, D, true>, grid, 32 * kAppendWarps, s, a)
                 : launch(k_cache_append<T, E4M3, D, false>, grid, 32 * kAppendWarps, s, a);

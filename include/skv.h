@@ -411,8 +411,8 @@ skv_status skv_decode_attn_noalloc(const void *q, skv_dtype dtype, int B, int R,
  * page_table : [B][max_pages] int32 page ids; position t of sequence b lies in page
  *              page_table[b][t / 64], slot t % 64. Sequences may share pages that none appends to.
  * lens       : [B] int32 tokens held.
- * The pages pointer must be 16-byte aligned; num_pages at most INT32_MAX, max_pages * 64 at most
- * 2^30, Hkv at most 65,535. Slots behind a sequence's last token are never read into a result: they
+ * The pages pointer must be 16-byte aligned; num_pages * Hkv * 4 at most INT32_MAX, max_pages * 64
+ * at most 2^30, Hkv at most 65,535. Slots behind a sequence's last token are never read into a result: they
  * may hold anything.
  */
 #define SKV_CACHE_PAGE_TOKENS 64

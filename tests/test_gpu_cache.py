@@ -82,6 +82,33 @@ def test_append_writes_what_the_definition_says(dtype, fmt, d, Hkv, fused):
     assert torch.equal(a, w)
 
 
+@pytest.mark.parametrize("dtype,fmt", [(BF, "e4m3"), (BF, "raw"), (F32, "e4m3")])
+@pytest.mark.parametrize("d,Hkv,n", [(128, 4, 24000), (64, 8, 33001), (64, 3, 40007), (128, 1, 50021), (128, 12, 9999)])
+def test_append_long_prompts(dtype, fmt, d, Hkv, n):
+    """Enough rows that every warp takes several: read back, they are the rows quantised by torch's own e4m3
+    conversion (which the host tests compare with the definition)."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    cut = n // 3
+    cache, table = make(2, Hkv, d, dtype, fmt, [cut + 7, n - cut], seed=1)
+    x = (torch.randn(n + 5, Hkv + 1, 2 * d, generator=g, device="cuda") * torch.exp(3 * torch.randn(n + 5, 1, 1, generator=g, device="cuda"))).to(dtype)
+    k, v = x[:, :Hkv, :d], x[:, 1:, d:]
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = skv.cache_append(k, v, cache, table, i32([7, 0]), cu_new=i32([0, cut, n]), workspace=ws)
+    assert got.tolist() == [cut + 7, n - cut]
+    rk, rv = skv.cache_read(cache, table, [7, 0], [cut, n - cut], workspace=ws)
+    ok(ws)
+    for src, have in ((k, rk), (v, rv)):
+        want = src[:n].float()
+        if fmt == "e4m3":
+            a = want.abs().amax(-1)
+            m, p = torch.frexp(a)
+            e = torch.where(m > 0.875, p - 8, p - 9).clamp(-100, 119)
+            two = ((torch.stack([e, -e]).int() + 127) << 23).view(torch.float32)
+            want = (want * two[1][..., None]).to(torch.float8_e4m3fn).float() * two[0][..., None]
+        want = torch.cat([want[:cut].transpose(0, 1).reshape(-1, d), want[cut:].transpose(0, 1).reshape(-1, d)])
+        assert torch.equal(have, want.to(dtype))
+
+
 def test_append_special_values():
     """Zeros, subnormals, the largest finite values, infinities and NaN; ties go to the even code."""
     d = 64
