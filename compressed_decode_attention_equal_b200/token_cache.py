@@ -11,6 +11,7 @@ one launch on the current stream of the tensors' device (or on `stream`). There 
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 
@@ -241,9 +242,13 @@ def _int_array(n: int):
 
 def _int32s(values, name: str):
     """A C array of host integers (ctypes alone would cut them to 32 bits)."""
-    if not (0 <= min(values) and max(values) < 1 << 31):
+    try:
+        got = array.array("i", values)
+    except OverflowError:
+        got = (-1,)
+    if min(got) < 0:
         raise ValueError(f"{name} must be integers from 0 to 2^31 - 1")
-    return _int_array(len(values))(*map(int, values))
+    return _int_array(len(got)).from_buffer(got)
 
 
 def paged_attn_workspace_bytes(B: int, R: int, Hq: int, Hkv: int, d: int, max_pages: int) -> int:

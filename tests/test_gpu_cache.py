@@ -353,11 +353,18 @@ def test_attention_many_short_units(dtype, fmt, d, B, Hkv, G):
         ref.check_attention(out[b], lse[b], reference(q, cache, table, lens, b), dtype, fmt, f"sequence {b}")
     # the rest against the same rows in plain torch, all at once
     (k, v), _ = ref.read_rows(cache, [0], 0, 41)
-    k, v = (torch.from_numpy(t).cuda().permute(1, 0, 2) for t in (k, v))
-    s = torch.einsum("bhgd,htd->bhgt", q.double().view(B, Hkv, G, d), k) / math.sqrt(d)
-    s = s.masked_fill(torch.arange(41, device="cuda") >= i32(lens)[:, None, None, None], -math.inf)
-    # the bounds of cache_reference.attention_bounds, row by row (the 2^-25 of tiny weights goes into 2^-16)
-    size = torch.einsum("bhgd,htd->bhgt", q.double().view(B, Hkv, G, d).abs(), k.abs()).amax(-1) / math.sqrt(d)
+    check_shared(out, lse, q, *(torch.from_numpy(t).cuda().permute(1, 0, 2) for t in (k, v)), lens, dtype, fmt)
+
+
+def check_shared(out, lse, q, k, v, lens, dtype, fmt):
+    """Sequences that share their keys k, v [Hkv, t, d] (fp64), each seeing the first lens[b], within the bounds of
+    cache_reference.attention_bounds, row by row (the 2^-25 of tiny weights goes into 2^-15)."""
+    B, _, Hq, d = q.shape
+    Hkv, T, _ = k.shape
+    x = q.double().view(B, Hkv, Hq // Hkv, d)
+    seen = torch.arange(T, device="cuda") < i32(lens)[:, None, None, None]
+    s = (torch.einsum("bhgd,htd->bhgt", x, k) / math.sqrt(d)).masked_fill(~seen, -math.inf)
+    size = torch.einsum("bhgd,htd->bhgt", x.abs(), k.abs()).amax(-1) / math.sqrt(d)
     dlogit = (2.0 ** -24 * (d + 12) * size + 2.0 ** -21).reshape(B, 1, -1)
     want = torch.logsumexp(s, -1).view(B, 1, -1)
     fin = want > -math.inf
@@ -369,6 +376,23 @@ def test_attention_many_short_units(dtype, fmt, d, B, Hkv, G):
     weight = 0.0 if dtype == F32 else 2.0 ** -11 if fmt == "e4m3" else 2.0 ** -8
     half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
     assert torch.all((out.double() - o).abs() <= mass * (weight + 2.0 ** -15 + 2 * dlogit[..., None]) * (1 + half) + half * o.abs() + 1e-30)
+
+
+@pytest.mark.parametrize("dtype,fmt,d,G", [(BF, "e4m3", 128, 1), (BF, "raw", 128, 7), (BF, "e4m3", 64, 8), (BF, "e4m3", 128, 12),
+                                           (BF, "raw", 64, 28), (F32, "raw", 64, 2), (F32, "e4m3", 128, 3)])
+def test_attention_many_long_units(dtype, fmt, d, G):
+    """Pieces of more groups than a warp looks page ids up for at once: 48 sequences of up to 8,192 tokens that share
+    their pages (one prefix), 8 KV heads."""
+    B, Hkv, T = 48, 8, 8192
+    lens = [T - 61 * b for b in range(B)]
+    cache, table = make(1, Hkv, d, dtype, fmt, [T], seed=4)
+    g = torch.Generator(device="cuda").manual_seed(d + G)
+    k, v = (torch.randn(T, Hkv, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    skv.cache_append(k, v, cache, table, i32([0]))
+    k, v = skv.cache_read(cache, table, [0], [T])
+    q = torch.randn(B, 1, G * Hkv, d, generator=g, device="cuda").to(dtype)
+    out, lse = skv.paged_attn(q, cache, table.expand(B, -1).contiguous(), i32(lens))
+    check_shared(out, lse, q, k.view(Hkv, T, d).double(), v.view(Hkv, T, d).double(), lens, dtype, fmt)
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "raw"])
