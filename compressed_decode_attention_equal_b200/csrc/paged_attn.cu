@@ -13,6 +13,9 @@ namespace skv {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kSlack = 8.f;                  // 2^8 times a value's scale, 2^119 at most, stays within fp32
+constexpr float kSpan = 126.f;                 // 2^126 stays finite, and 2^-126 is the smallest normal output
+constexpr float kNoLogit = -3.402823466e38f;   // no maximum yet: finite, so that a masked logit (-inf) less it is not NaN
 
 // cap tanh(t) in front of 16-bit products: tanh t = 1 - 2 / (e^(2t) + 1), whose absolute error stays within a few
 // ulps of 1 over the whole range (the hardware tanh's 2^-11 would show in the logits)
@@ -45,7 +48,7 @@ struct MmaSmem {
     float o[kOut > kJoin ? kOut : kJoin];        // kTurn tiles of all warps: [kTurn][W][4 D / 16][kMerge]
     alignas(16) uint8_t q[kRows][kQRow];
     float qfac[kRows], slope[kRows];
-    float m[W][kRows], l[W][kRows], part[kRows];
+    float m[W][kRows], mw[E4M3 ? W : 1][kRows], l[W][kRows], part[kRows];
     alignas(8) uint64_t full[W][S];
     PagedSched sched;
 };
@@ -205,16 +208,16 @@ struct GroupRing {
 //   Keys: the contraction order over d is free as long as keys and queries agree; a lane's 16
 //   bytes of a key row serve several steps, so that a group's keys are 4 (e4m3) or 8 (raw) 16-byte loads.
 //   Values: transposed on load by byte permutes of neighbouring tokens' words.
-//   e4m3: codes go to fp16 (exact); a query row is scaled by a power of two into fp16's range, exactly;
-//   the key's scale multiplies the logit, the value's exponent is added to the base-2 logit before the
-//   maximum is taken, so that the fp16 weight 2^(s + ve - max) holds the value's scale too, and the
-//   partition sums 2^(s + ve - max) 2^-ve.
+//   e4m3: codes go to fp16 (exact); a query row is scaled by a power of two into fp16's range, exactly; the key's
+//   scale multiplies the logit, and the value's the weight: the fp16 weight is 2^(s + ve - mw), with mw the
+//   running maximum of base-2 logit + value exponent, beside m, the logits' own, for the partition sum 2^(s - m).
+//   So neither a value's scale nor a value of zeros can take precision from the partition or the other values.
 //   Weights are rounded to the matrix type (fp16 2^-11, bf16 2^-8 relative): the second product runs on
-//   16-bit operands, and the partition keeps the fp32 weights. Sums and maxima are fp32. The reference maximum
-//   moves only when a logit exceeds it by 2^8, so that the rescale of O runs rarely.
+//   16-bit operands, and the partition keeps the fp32 weights. Sums and maxima are fp32. A reference maximum
+//   moves only when it is exceeded by 8 (2^8), so that the rescale of O runs rarely.
 // Measured: 32 sequences x 4 heads x 32,768 e4m3 keys at 7 rows take 172 us, 97% of the copy rate (raw, ragged:
 // 79.5 us, 94%). An mma.sync, a conversion and an FMA add up on one scheduler here instead of overlapping, so
-// that many rows are bound by the instruction rate: 28 rows over 8 x 4 x 16,384 e4m3 keys take 61 us, 34%.
+// that many rows are bound by the instruction rate: 28 rows over 8 x 4 x 16,384 e4m3 keys take 66 us, 32%.
 template <bool E4M3, int D, int NT, int W, int S, int CTAS, int TP>
 __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
     using Sm = MmaSmem<E4M3, D, NT, W, S, CTAS, TP>;
@@ -318,14 +321,14 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) qf[ks] = qfrag(0, ks);
         }
-        float fac[NT][2], slope[NT][2], mref[NT][2], l[NT][2], o[NT][MT][4];
+        float fac[NT][2], slope[NT][2], mref[NT][2], mw[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 fac[nt][c] = sm.qfac[8 * nt + 2 * tq + c];
                 slope[nt][c] = sm.slope[8 * nt + 2 * tq + c];
-                mref[nt][c] = -3.402823466e38f;   // finite: a masked logit (-inf) less it is -inf, not NaN
+                mref[nt][c] = mw[nt][c] = kNoLogit;
                 l[nt][c] = 0.f;
             }
 #pragma unroll
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) s[0][c] += s2[c];
                     }
-                    float ve[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};
+                    float ve[2] = {0.f, 0.f}, vs[2] = {1.f, 1.f};   // a value's exponent and scale
                     float ksc[2] = {1.f, 1.f};
                     if constexpr (E4M3) {
 #pragma unroll
@@ -391,13 +394,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                             const uint32_t vb = buf[2 * G::kBlock + kGroupTokens + g + 8 * c];
                             ksc[c] = scale_of(kb);
                             ve[c] = static_cast<float>(static_cast<int>(vb) - 127);
-                            vinv[c] = scale_of(254 - vb);
+                            vs[c] = scale_of(vb);
                         }
                     }
                     const float gap0 = static_cast<float>(hi - 1 - t0 - g);
                     const bool partial = t0 < lo || t0 + kGroupTokens > hi;
                     const bool in0 = t0 + g >= lo && t0 + g < hi, in1 = t0 + g + 8 >= lo && t0 + g + 8 < hi;
-                    bool raise = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -405,9 +407,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                             float x = s[nt][c] * fac[nt][c & 1];
                             if constexpr (E4M3) x *= ksc[c >> 1];
                             if (a.softcap > 0.f) x = capped(x, cap_l2);
-                            x = fmaf(-slope[nt][c & 1], gap0 - 8.f * (c >> 1), x);
-                            if constexpr (E4M3) x += ve[c >> 1];
-                            s[nt][c] = x;
+                            s[nt][c] = fmaf(-slope[nt][c & 1], gap0 - 8.f * (c >> 1), x);
                         }
                     if (partial) {
 #pragma unroll
@@ -415,25 +415,56 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                             if (!in0) s[nt][0] = s[nt][1] = -INFINITY;
                             if (!in1) s[nt][2] = s[nt][3] = -INFINITY;
                         }
-                        if (!in0) vinv[0] = 0.f;   // an exponent byte behind the end may be anything
-                        if (!in1) vinv[1] = 0.f;
+                        if (!in0) vs[0] = 0.f;   // an exponent byte behind the end may be anything
+                        if (!in1) vs[1] = 0.f;
                     }
+                    // The reference maxima: of the logits for the partition and, e4m3, of logit + value exponent for the
+                    // weights of the outputs. Both move only when one is exceeded by kSlack (or may be: the larger
+                    // of a lane's two exponents stands for both).
+                    float over = -INFINITY;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) raise |= s[nt][c] > mref[nt][c & 1] + 8.f;
-                    if (__any_sync(0xffffffffu, raise)) {
+                        for (int c = 0; c < 2; ++c) {
+                            const float m = E4M3 ? fminf(mref[nt][c], mw[nt][c] - fmaxf(ve[0], ve[1])) : mref[nt][c];
+                            over = fmaxf(over, fmaxf(s[nt][c], s[nt][c + 2]) - m);
+                        }
+                    if (__any_sync(0xffffffffu, over > kSlack)) {
+                        if (E4M3 && __any_sync(0xffffffffu, ve[0] == 0.f || ve[1] == 0.f)) {
+                            // a value of zeros is held with exponent 0, which must not set the scale that the other
+                            // values' weights are rounded at
+                            const uint32_t at = base + G::kBlock + (lane >> 1) * G::kVec + (lane & 1) * (G::kVec / 2);
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int i = 0; i < G::kVec / 32; ++i) {
+                                const uint4 u = lds128(at + 16 * i);
+                                any |= u.x | u.y | u.z | u.w;
+                            }
+                            const uint32_t empty = __ballot_sync(0xffffffffu, (any & 0x7f7f7f7fu) == 0);   // half vectors
+                            const uint32_t zero = empty & empty >> 1 & 0x55555555u;
+                            if (zero >> 2 * g & 1) ve[0] = -INFINITY, vs[0] = 0.f;
+                            if (zero >> 2 * (g + 8) & 1) ve[1] = -INFINITY, vs[1] = 0.f;
+                        }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 float top = fmaxf(s[nt][c], s[nt][c + 2]);
+                                float topw = fmaxf(s[nt][c] + ve[0], s[nt][c + 2] + ve[1]);
 #pragma unroll
-                                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                                for (int x = 4; x < 32; x <<= 1) {
+                                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                                    if constexpr (E4M3) topw = fmaxf(topw, __shfl_xor_sync(0xffffffffu, topw, x));
+                                }
                                 top = fmaxf(top, mref[nt][c]);
-                                const float f = ex2(mref[nt][c] - top);
-                                mref[nt][c] = top;
+                                float f = ex2(mref[nt][c] - top);
                                 l[nt][c] *= f;
+                                mref[nt][c] = top;
+                                if constexpr (E4M3) {
+                                    topw = fmaxf(fmaxf(topw, mw[nt][c]), top - kSpan);   // zeros only so far: finite
+                                    f = ex2(mw[nt][c] - topw);
+                                    mw[nt][c] = topw;
+                                }
 #pragma unroll
                                 for (int j = 0; j < MT; ++j) o[nt][j][c] *= f, o[nt][j][c + 2] *= f;
                             }
@@ -442,11 +473,13 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float p[4];
+                        float rw[2] = {1.f, 1.f};   // from the partition's reference to the outputs'
+                        if constexpr (E4M3) rw[0] = ex2(mref[nt][0] - mw[nt][0]), rw[1] = ex2(mref[nt][1] - mw[nt][1]);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             p[c] = ex2(s[nt][c] - mref[nt][c & 1]);
-                            if constexpr (E4M3) l[nt][c & 1] = fmaf(p[c], vinv[c >> 1], l[nt][c & 1]);
-                            else l[nt][c & 1] += p[c];
+                            l[nt][c & 1] += p[c];
+                            if constexpr (E4M3) p[c] = p[c] * vs[c >> 1] * rw[c & 1];   // in this order within fp32's range
                         }
                         pb[nt][0] = movmatrix_t(E4M3 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
                         pb[nt][1] = movmatrix_t(E4M3 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
@@ -517,12 +550,13 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                 for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
                 if (g == 0) {
                     sm.m[warp][8 * nt + 2 * tq + c] = mref[nt][c];
+                    if constexpr (E4M3) sm.mw[warp][8 * nt + 2 * tq + c] = mw[nt][c];
                     sm.l[warp][8 * nt + 2 * tq + c] = sum;
                 }
             }
         __syncthreads();
         static_assert(ROWS * W <= THREADS && (W & (W - 1)) == 0, "one lane per row and warp");
-        if (tid < ROWS * W) {   // the warps' weights, 2^(m - largest m) over the joint sum, and the row's partition
+        if (tid < ROWS * W) {   // the warps' weights, 2^(mw - largest m) over the joint sum, and the row's partition
             const int r = tid / W, w = tid % W;
             const float mine = sm.m[w][r];
             float top = mine;
@@ -532,7 +566,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
             float sum = f * sm.l[w][r];
 #pragma unroll
             for (int x = 1; x < W; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            sm.m[w][r] = sum == 0.f ? 0.f : f * __frcp_rn(sum);
+            sm.m[w][r] = sum == 0.f ? 0.f : (E4M3 ? ex2(sm.mw[E4M3 ? w : 0][r] - top) : f) * __frcp_rn(sum);
             if (w == 0) sm.part[r] = sum == 0.f ? -INFINITY : top + __log2f(sum);
         }
         // one copy of this code for all tiles: each turn writes the first kTurn and moves the others down

@@ -120,8 +120,10 @@ class Attn:
             self.lse[:, h] = (top + np.log(z))[:, 0]
             self.out[:, h] = p @ vv
             self.mass[:, h] = p @ np.abs(vv)
-            # a 16-bit weight of 2^-14 of the largest (scaled by its value's scale) or less is off by 2^-25 of it
-            self.tiny[:, h] = 2.0 ** -25 * (p * vs).max(-1, keepdims=True) * (np.abs(vv) / vs[:, None]).sum(0)
+            # a 16-bit weight of 2^-14 of the largest (scaled by its value's scale) or less is off by 2^-25 of it;
+            # values of zeros have no scale
+            some = np.abs(vv).max(-1) > 0
+            self.tiny[:, h] = 2.0 ** -25 * (p * vs * some).max(-1, keepdims=True) * (np.abs(vv) / vs[:, None]).sum(0)
             # d products and sums, the scales, the cap (a few 2^-24 of itself and of the cap) and the bias, each
             # rounded in fp32, and the exponent's base-2 conversion
             self.dlogit[:, h] = (2.0 ** -24 * ((d + 8) * size.max(-1) + 16 * softcap + 8 * np.abs(np.asarray(bias)).max()

@@ -419,6 +419,48 @@ def test_attention_peaked_and_unequal_scales(fmt):
         ref.check_attention(out[b], lse[b], reference(q, cache, table, [n] * 3, b), BF, fmt, f"row {b}")
 
 
+@pytest.mark.parametrize("dtype,fmt", [(BF, "e4m3"), (BF, "raw"), (F32, "e4m3")])
+@pytest.mark.parametrize("d,G,size", [(128, 7, 2.0 ** -30), (64, 2, 2.0 ** -60), (128, 12, 2.0 ** -10), (64, 28, 2.0 ** 40)])
+def test_values_of_zeros_leave_small_values_alone(dtype, fmt, d, G, size):
+    """Keys with the largest logits whose values are all zeros (of either sign) beside values far below and above 1: the
+    zeros add to the partition and to nothing else."""
+    n, Hkv = 333, 1
+    g = torch.Generator().manual_seed(d + G)
+    k, v = torch.randn(n, Hkv, d, generator=g), torch.randn(n, Hkv, d, generator=g) * size
+    q = torch.randn(2, 1, G, d, generator=g)
+    q[0] = q[0, 0, 0]
+    k[[0, 50, 200]] = 0.3 * q[0, 0, 0]                      # far above the others for the first sequence's rows
+    v[[0, 50, 120, 200, 332]] = 0.0
+    v[200] = -v[200]
+    cache, table = make(2, Hkv, d, dtype, fmt, [n] * 2)
+    for b in range(2):
+        skv.cache_append(k.to(dtype).cuda(), v.to(dtype).cuda(), cache, table[b:b + 1], i32([0]))
+    q = q.to(dtype).cuda()
+    out, lse = skv.paged_attn(q, cache, table, i32([n] * 2))
+    for b in range(2):
+        ref.check_attention(out[b], lse[b], reference(q, cache, table, [n] * 2, b), dtype, fmt, f"sequence {b}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,G", [(128, 7), (64, 12)])
+@pytest.mark.parametrize("at", [0, 20, 299])
+@pytest.mark.parametrize("gap,top,rest", [(80, 0.0, 1.0), (200, 0.0, 1.0), (180, 2.0 ** -100, 2.0 ** 110), (5, 2.0 ** 110, 2.0 ** -90)])
+def test_values_of_scales_far_apart(dtype, d, G, at, gap, top, rest):
+    """One key whose logit is `gap` above the others', which are about equal, and values of scales at the two ends of the
+    format's range, or zeros: finite results, none of them lost."""
+    n = 300
+    g = torch.Generator().manual_seed(at + G)
+    k, v = torch.randn(n, 1, d, generator=g) / 64, torch.randn(n, 1, d, generator=g) * rest
+    q = torch.ones(1, 1, G, d)
+    k[at] = gap / math.sqrt(d)
+    v[at] = torch.randn(1, d, generator=g) * top
+    cache, table = make(1, 1, d, dtype, "e4m3", [n])
+    skv.cache_append(k.to(dtype).cuda(), v.to(dtype).cuda(), cache, table, i32([0]))
+    q = q.to(dtype).cuda()
+    out, lse = skv.paged_attn(q, cache, table, i32([n]))
+    ref.check_attention(out[0], lse[0], reference(q, cache, table, [n], 0), dtype, "e4m3")
+
+
 @pytest.mark.parametrize("dtype,fmt", [(BF, "e4m3"), (BF, "raw"), (F32, "raw")])
 def test_nan_stays_where_it_is_seen(dtype, fmt):
     """A NaN key or value poisons the rows that see it and no other; behind the window, before `first` and behind
