@@ -35,8 +35,8 @@ struct MmaSmem {
     using G = CacheGeom<__nv_bfloat16, E4M3, D>;
     static constexpr int kStage = (TP * G::kGroup + 127) / 128 * 128;
     static constexpr int kRows = 8 * NT;
-    // rounds that a unit's query load and outputs take as long as: 1, 2, 3 measured 88.1, 73.5, 75.4 us with one row
-    // (64 ragged sequences x 16 heads), and 1, 2, 3, 4 with 28 rows 56.5, 47.3, 48.2, 46.8 us (48 x 4 heads)
+    // rounds that a unit's query load and outputs take as long as: 1, 2, 3 measured 89.8, 77.5, 80.3 us with one row
+    // (64 ragged sequences x 16 heads), and 1, 2, 3, 4 with 28 rows 58.6, 49.6, 50.2, 49.3 us (48 x 4 heads)
     static constexpr int kCost = NT == 1 ? 2 : 4;
     static constexpr int kQRow = 2 * D + 8;      // bytes of a query row: 8 more than 2 D against bank conflicts
     static constexpr int kMerge = 33;            // words per accumulator element of a warp's 32 lanes
@@ -959,12 +959,12 @@ cudaError_t launch_mma(const PagedArgs &a, cudaStream_t s) {
 template <bool E4M3, int D>
 cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     // at d = 64 two groups make a tile, which halves what a tile costs beside its products: 32 x 8 heads x 8,192 keys
-    // 70.9 -> 61.9 us (e4m3), 93.9 -> 86.7 us (raw)
+    // 74.0 -> 65.5 us (e4m3), 94.1 -> 87.1 us (raw)
     constexpr int TP = D == 64 ? 2 : 1;
     // Warps and CTAs per SM. e4m3, 8 rows: two CTAs of 8 warps at 128 registers (7B batch 172 us; one CTA of 8 warps
-    // 219 us: too few to hide a tile's latency). Raw tiles are twice the bytes for the same work: one CTA of 8
-    // warps (79.3 us; two of 4 84.7). More rows need the registers: 16 and 28 rows 45.0 and 61.0 us; with three
-    // and two CTAs of 4 warps 48.2 and 69.3.
+    // 223 us: too few to hide a tile's latency). Raw tiles are twice the bytes for the same work: one CTA of 8
+    // warps (79.3 us; two of 4 84.7). More rows need the registers: 16 and 28 rows 46.4 and 65.9 us; with three
+    // and two CTAs of 4 warps 49.3 and 75.5.
     if constexpr (E4M3) {
         if (a.pass_rows == 8) return launch_mma<E4M3, D, 1, 8, 2, 2, TP>(a, s);
         if (a.pass_rows == 16) return launch_mma<E4M3, D, 2, 8, 3, 1, TP>(a, s);
