@@ -316,10 +316,13 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
             const int d0 = E4M3 ? 64 * (ks / 4) + 16 * tq + 4 * (ks % 4) : 32 * (ks / 2) + 8 * tq + 4 * (ks % 2);
             return *reinterpret_cast<const uint2 *>(sm.q[8 * nt + g] + 2 * d0);
         };
-        uint2 qf[NT == 1 ? KS : 1];
-        if constexpr (NT == 1) {
+        constexpr bool QREG = NT <= 2;   // the queries stay in registers (16 rows: 46.5 -> 45.0 us; 28 would spill)
+        uint2 qf[QREG ? NT : 1][QREG ? KS : 1];
+        if constexpr (QREG) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) qf[ks] = qfrag(0, ks);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) qf[nt][ks] = qfrag(nt, ks);
         }
         float fac[NT][2], slope[NT][2], mref[NT][2], mw[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
@@ -370,12 +373,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                             }
                             const int ks = STEPS * i + w;
                             if constexpr (NT == 1) {   // two chains
-                                if (w & 1) mma_tile<E4M3>(s2, a0, a1, a2, a3, qf[ks].x, qf[ks].y);
-                                else mma_tile<E4M3>(s[0], a0, a1, a2, a3, qf[ks].x, qf[ks].y);
+                                if (w & 1) mma_tile<E4M3>(s2, a0, a1, a2, a3, qf[0][ks].x, qf[0][ks].y);
+                                else mma_tile<E4M3>(s[0], a0, a1, a2, a3, qf[0][ks].x, qf[0][ks].y);
                             } else {
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
-                                    const uint2 b = qfrag(nt, ks);
+                                    const uint2 b = QREG ? qf[QREG ? nt : 0][QREG ? ks : 0] : qfrag(nt, ks);
                                     mma_tile<E4M3>(s[nt], a0, a1, a2, a3, b.x, b.y);
                                 }
                             }
@@ -963,7 +966,7 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     constexpr int TP = D == 64 ? 2 : 1;
     // Warps and CTAs per SM. e4m3, 8 rows: two CTAs of 8 warps at 128 registers (7B batch 172 us; one CTA of 8 warps
     // 223 us: too few to hide a tile's latency). Raw tiles are twice the bytes for the same work: one CTA of 8
-    // warps (79.3 us; two of 4 84.7). More rows need the registers: 16 and 28 rows 46.4 and 65.9 us; with three
+    // warps (79.3 us; two of 4 84.7). More rows need the registers: 16 and 28 rows 45.0 and 65.9 us; with three
     // and two CTAs of 4 warps 49.3 and 75.5.
     if constexpr (E4M3) {
         if (a.pass_rows == 8) return launch_mma<E4M3, D, 1, 8, 2, 2, TP>(a, s);
