@@ -78,63 +78,30 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
-// The tiles of TT tokens that one warp of a CTA takes, in order, over the pieces of the table: what runs
-// ahead of the computation to issue the copies. The lanes hold the page ids of the next 32 tiles of a
-// piece, loaded together.
-template <int W, int TT>
-struct Feeder {
-    int i;                 // piece of the table; the table's n: no more tiles
-    int g, g_end, ids, at; // this tile, the piece's end, lane j: page id of the j-th tile after the load, tiles since
-
-    __device__ __forceinline__ void load_ids(const PagedArgs &a, const PagedSched &s) {
-        const int mine = g + W * static_cast<int>(threadIdx.x & 31);
-        ids = mine < g_end ? ld_global_s32(a.page_table + static_cast<int64_t>(s.piece[i].b) * a.max_pages + mine / (SKV_CACHE_PAGE_TOKENS / TT))
-                           : -1;
-        at = 0;
-    }
-    __device__ __forceinline__ int page() const { return __shfl_sync(0xffffffffu, ids, at); }
-    // to the first tile of piece i or, where this warp has none there, of the pieces after it
-    __device__ __forceinline__ void settle(const PagedArgs &a, const PagedSched &s, int warp) {
-        for (; i < s.n; ++i) {
-            const PagedPiece &p = s.piece[i];
-            const int g0 = p.lo / TT;
-            g = g0 + p.r0 * W + warp;
-            g_end = p.hi > p.lo ? min((p.hi + TT - 1) / TT, g0 + p.r1 * W) : 0;
-            if (g < g_end) break;
-        }
-        if (i < s.n) load_ids(a, s);
-    }
-    __device__ __forceinline__ void step(const PagedArgs &a, const PagedSched &s, int warp) {
-        g += W;
-        if (++at == 32 && g < g_end) load_ids(a, s);
-        if (g >= g_end) {
-            ++i;
-            settle(a, s, warp);
-        }
-    }
-};
-
 // One warp's ring of S stages, a tile of TP token groups each (neighbours of one page): copies are issued S
-// tiles ahead of the computation, one bulk copy per tile, and across piece ends. A tile on a bad page is
-// reported and skipped. When a wait gives up the warp issues and waits for nothing more (bar the copies
-// in flight, at the end).
+// tiles ahead of the computation, one bulk copy per tile, and across piece ends. The warp takes every W-th tile
+// of the table's pieces, in order, 32 tiles of a piece at a time: lane j looks up the page of the j-th and
+// issues its copy. A tile on a bad page is reported and skipped. When a wait gives up the warp issues and waits
+// for nothing more (bar the copies in flight, at the end).
 template <int W, int S, int TP, int GROUP, int STAGE>
 struct GroupRing {
-    static constexpr int BYTES = TP * GROUP;
+    static constexpr int BYTES = TP * GROUP, TT = TP * kGroupTokens;
     uint8_t *buf;           // [S][STAGE]
     uint64_t *full;         // [S]
-    Feeder<W, TP * kGroupTokens> feed;
+    int i, g, g_end;        // piece of the table, first of the 32 tiles, the piece's end
+    int group;              // this lane's tile: its first group in the pool
+    int at, count;          // tiles issued of how many (0: there are no more)
+    uint32_t bad;           // lanes whose tile's page id is bad
     uint32_t skip;          // stages whose tile's page id is bad: nothing was copied
-    uint32_t pending;       // stages with a copy that has not been waited for
     uint32_t phase;
-    int stage;
+    int stage, ahead;       // ahead: stages from this one on that have been issued
     bool dead;
 
     __device__ __forceinline__ void init(uint8_t *ring, uint64_t *bars) {
         buf = ring;
         full = bars;
-        skip = pending = phase = 0;
-        stage = 0;
+        skip = phase = 0;
+        stage = ahead = 0;
         dead = false;
         if ((threadIdx.x & 31) == 0) {
             for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
@@ -142,43 +109,74 @@ struct GroupRing {
         }
         __syncwarp();
     }
+    __device__ __forceinline__ void look_up(const PagedArgs &a, const PagedSched &sched) {
+        const PagedPiece &p = sched.piece[i];
+        const int tile = g + W * static_cast<int>(threadIdx.x & 31);
+        int page = 0;
+        if (tile < g_end) page = ld_global_s32(a.page_table + static_cast<int64_t>(p.b) * a.max_pages + tile / (kPageGroups / TP));
+        count = min((g_end - g + W - 1) / W, 32);
+        bad = __ballot_sync(0xffffffffu, tile < g_end && (page < 0 || page >= a.num_pages));
+        group = (page * a.Hkv + p.h) * kPageGroups + tile % (kPageGroups / TP) * TP;   // a pool's groups stay below 2^31
+        at = 0;
+    }
+    // to the first tile of piece i or, where this warp has none there, of the pieces after it
+    __device__ __forceinline__ void settle(const PagedArgs &a, const PagedSched &sched) {
+        for (; i < sched.n; ++i) {
+            const PagedPiece &p = sched.piece[i];
+            const int g0 = p.lo / TT;
+            g = g0 + p.r0 * W + static_cast<int>(threadIdx.x >> 5);
+            g_end = p.hi > p.lo ? min((p.hi + TT - 1) / TT, g0 + p.r1 * W) : 0;
+            if (g < g_end) return look_up(a, sched);
+        }
+        at = count = 0;
+    }
     __device__ __forceinline__ void issue(const PagedArgs &a, const PagedSched &sched, int s) {
-        if (feed.i >= sched.n || dead) return;
-        const bool leader = (threadIdx.x & 31) == 0;
-        const int page = feed.page();
-        if (page < 0 || page >= a.num_pages) {
-            if (leader) {
+        if (at >= count) return;
+        const bool mine = (threadIdx.x & 31) == at;
+        if (bad | skip) {
+            const bool none = bad >> at & 1;
+            skip = none ? skip | 1u << s : skip & ~(1u << s);
+            if (mine && none) {
                 raise_flag(a.flags, FLAG_BAD_PAGE);
                 mbar_arrive(&full[s]);
             }
-            skip |= 1u << s;
-        } else {
-            skip &= ~(1u << s);
-            if (leader) {
-                const int64_t group = (static_cast<int64_t>(page) * a.Hkv + sched.piece[feed.i].h) * kPageGroups + feed.g % (kPageGroups / TP) * TP;
-                mbar_arrive_expect_tx(&full[s], BYTES);
-                bulk_g2s(buf + s * STAGE, a.pages + group * GROUP, BYTES, &full[s]);
+        }
+        if (mine && !(bad >> at & 1)) {
+            mbar_arrive_expect_tx(&full[s], BYTES);
+            bulk_g2s(buf + s * STAGE, a.pages + static_cast<int64_t>(group) * GROUP, BYTES, &full[s]);
+        }
+        ++ahead;
+        if (++at == count) {
+            g += 32 * W;
+            if (g < g_end) {
+                look_up(a, sched);
+            } else {
+                ++i;
+                settle(a, sched);
             }
         }
-        pending |= 1u << s;
-        feed.step(a, sched, threadIdx.x >> 5);
     }
     // a new piece table: nothing is in flight
     __device__ __forceinline__ void begin(const PagedArgs &a, const PagedSched &sched) {
-        feed.i = 0;
-        feed.settle(a, sched, threadIdx.x >> 5);
+        i = 0;
+        settle(a, sched);
+        if (dead) count = 0;
 #pragma unroll 1
         for (int s = 0; s < S; ++s) issue(a, sched, stage + s < S ? stage + s : stage + s - S);
     }
     // false: nothing to compute (a wait gave up; the stage stays)
     __device__ __forceinline__ bool wait(const PagedArgs &a) {
-        if (!dead && !mbar_wait(&full[stage], phase)) {
-            dead = true;
-            if ((threadIdx.x & 31) == 0) raise_flag(a.flags, FLAG_TIMEOUT);
+        if (dead) return false;
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&full[stage], phase))) {
+            dead = !__all_sync(0xffffffffu, mbar_wait(&full[stage], phase));
+            if (dead) {
+                if ((threadIdx.x & 31) == 0) raise_flag(a.flags, FLAG_TIMEOUT);
+                count = 0;
+                return false;
+            }
         }
-        dead = __any_sync(0xffffffffu, dead);
-        if (!dead) pending &= ~(1u << stage);
-        return !dead;
+        --ahead;
+        return true;
     }
     __device__ __forceinline__ bool skipped() const { return skip >> stage & 1; }
     __device__ __forceinline__ const uint8_t *data() const { return buf + stage * STAGE; }
@@ -191,8 +189,10 @@ struct GroupRing {
     // a warp that gave up leaves only when the copies that it issued have landed (bounded again)
     __device__ __forceinline__ void drain() {
         if (dead)
-            for (int s = 0; s < S; ++s)
-                if (pending >> s & 1) mbar_wait(&full[s], s < stage ? phase ^ 1 : phase);
+            for (int j = 0; j < ahead; ++j) {
+                const int s = stage + j < S ? stage + j : stage + j - S;
+                mbar_wait(&full[s], s < stage ? phase ^ 1 : phase);
+            }
     }
 };
 
