@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                             const uint32_t kb = buf[2 * G::kBlock + g + 8 * c];
                             const uint32_t vb = buf[2 * G::kBlock + kGroupTokens + g + 8 * c];
                             ksc[c] = scale_of(kb);
-                            ve[c] = static_cast<float>(static_cast<int>(vb) - 127);
+                            ve[c] = __uint_as_float(0x4b000000u | vb) - (8388608.f + 127.f);   // vb - 127
                             vs[c] = scale_of(vb);
                         }
                     }
@@ -409,9 +409,18 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                         for (int c = 0; c < 4; ++c) {
                             float x = s[nt][c] * fac[nt][c & 1];
                             if constexpr (E4M3) x *= ksc[c >> 1];
-                            if (a.softcap > 0.f) x = capped(x, cap_l2);
-                            s[nt][c] = fmaf(-slope[nt][c & 1], gap0 - 8.f * (c >> 1), x);
+                            s[nt][c] = x;
                         }
+                    if (a.softcap > 0.f) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) s[nt][c] = capped(s[nt][c], cap_l2);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[nt][c] = fmaf(-slope[nt][c & 1], gap0 - 8.f * (c >> 1), s[nt][c]);
                     if (partial) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
