@@ -72,6 +72,14 @@ __device__ __forceinline__ uint32_t cvt_lo(uint32_t w) { return e4m3x2_to_f16x2(
 __device__ __forceinline__ uint32_t cvt_hi(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16)); }
 __device__ __forceinline__ uint32_t word(const uint4 &u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 
+// Transposed load of two matrices of 16 rows x 16 bytes (lanes 0-15 and 16-31 give their rows' addresses): r[0] is column
+// lane / 4, r[1] column lane / 4 + 8 of the first, rows 4 (lane % 4) .. + 3; r[2], r[3] of the second.
+__device__ __forceinline__ void ldsm_t8(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -207,7 +215,7 @@ struct GroupRing {
 // and meets the other warps only at the end of a piece.
 //   Keys: the contraction order over d is free as long as keys and queries agree; a lane's 16
 //   bytes of a key row serve several steps, so that a group's keys are 4 (e4m3) or 8 (raw) 16-byte loads.
-//   Values: transposed on load by byte permutes of neighbouring tokens' words.
+//   Values: transposed by byte permutes of neighbouring tokens' words or, up to 8 rows of e4m3, by the load.
 //   e4m3: codes go to fp16 (exact); a query row is scaled by a power of two into fp16's range, exactly; the key's
 //   scale multiplies the logit, and the value's the weight: the fp16 weight is 2^(s + ve - mw), with mw the
 //   running maximum of base-2 logit + value exponent, beside m, the logits' own, for the partition sum 2^(s - m).
@@ -226,6 +234,12 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Sm &sm = *reinterpret_cast<Sm *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+    // Values transposed by the load instead of byte permutes: up to 8 rows 73.3 -> 72.2 us (64 x 16 heads) and 58.9 ->
+    // 54.9 (d = 64), where many warps hide its bank conflicts; 28 rows 62.4 -> 63.4. Then rows g, g + 8 of the
+    // logits' matrix are tokens tg, tg + 2, in the order that the load deals them out.
+    constexpr bool LDSM = E4M3 && NT == 1;
+    constexpr int TD = LDSM ? 2 : 8;
+    const int tg = LDSM ? 4 * (g >> 1) + (g & 1) : g;
     GroupRing<W, S, TP, G::kGroup, Sm::kStage> ring;
     ring.init(sm.ring[warp][0], sm.full[warp]);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -349,18 +363,18 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                     if (ring.skipped() || (TP > 1 && (t0 >= hi || t0 + kGroupTokens <= lo))) continue;
                     const uint8_t *buf = ring.data() + half * G::kGroup;
                     const uint32_t base = smem_u32(buf);
-                    // ---- logits: tokens g, g + 8 x rows 2 tq, 2 tq + 1 of every tile
+                    // ---- logits: tokens tg, tg + TD x rows 2 tq, 2 tq + 1 of every tile
                     float s[NT][4], s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
-                    const uint32_t krow = base + g * G::kVec;
+                    const uint32_t krow = base + tg * G::kVec;
                     constexpr int STEPS = E4M3 ? 4 : 2;   // steps that one 16-byte chunk serves
 #pragma unroll
                     for (int i = 0; i < KS / STEPS; ++i) {
-                        const uint32_t at = krow + 16 * cache_chunk(4 * i + tq, g, G::kChunks);
-                        const uint4 ka = lds128(at), kb = lds128(at + 8 * G::kVec);
+                        const uint4 ka = lds128(krow + 16 * cache_chunk(4 * i + tq, tg, G::kChunks));
+                        const uint4 kb = lds128(krow + TD * G::kVec + 16 * cache_chunk(4 * i + tq, tg + TD, G::kChunks));
 #pragma unroll
                         for (int w = 0; w < STEPS; ++w) {
                             uint32_t a0, a1, a2, a3;
@@ -393,16 +407,16 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                     if constexpr (E4M3) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const uint32_t kb = buf[2 * G::kBlock + g + 8 * c];
-                            const uint32_t vb = buf[2 * G::kBlock + kGroupTokens + g + 8 * c];
+                            const uint32_t kb = buf[2 * G::kBlock + tg + TD * c];
+                            const uint32_t vb = buf[2 * G::kBlock + kGroupTokens + tg + TD * c];
                             ksc[c] = scale_of(kb);
                             ve[c] = __uint_as_float(0x4b000000u | vb) - (8388608.f + 127.f);   // vb - 127
                             vs[c] = scale_of(vb);
                         }
                     }
-                    const float gap0 = static_cast<float>(hi - 1 - t0 - g);
+                    const float gap0 = static_cast<float>(hi - 1 - t0 - tg);
                     const bool partial = t0 < lo || t0 + kGroupTokens > hi;
-                    const bool in0 = t0 + g >= lo && t0 + g < hi, in1 = t0 + g + 8 >= lo && t0 + g + 8 < hi;
+                    const bool in0 = t0 + tg >= lo && t0 + tg < hi, in1 = t0 + tg + TD >= lo && t0 + tg + TD < hi;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -420,7 +434,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) s[nt][c] = fmaf(-slope[nt][c & 1], gap0 - 8.f * (c >> 1), s[nt][c]);
+                        for (int c = 0; c < 4; ++c) s[nt][c] = fmaf(-slope[nt][c & 1], gap0 - static_cast<float>(TD) * (c >> 1), s[nt][c]);
                     if (partial) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
@@ -454,8 +468,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                             }
                             const uint32_t empty = __ballot_sync(0xffffffffu, (any & 0x7f7f7f7fu) == 0);   // half vectors
                             const uint32_t zero = empty & empty >> 1 & 0x55555555u;
-                            if (zero >> 2 * g & 1) ve[0] = -INFINITY, vs[0] = 0.f;
-                            if (zero >> 2 * (g + 8) & 1) ve[1] = -INFINITY, vs[1] = 0.f;
+                            if (zero >> 2 * tg & 1) ve[0] = -INFINITY, vs[0] = 0.f;
+                            if (zero >> 2 * (tg + TD) & 1) ve[1] = -INFINITY, vs[1] = 0.f;
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -496,52 +510,74 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                         pb[nt][0] = movmatrix_t(E4M3 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
                         pb[nt][1] = movmatrix_t(E4M3 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
                     }
-                    // ---- outputs: tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 x this lane's d
-                    const uint32_t vrow = base + G::kBlock + 2 * tq * G::kVec;
-                    constexpr int HALVES = D * G::kElem / 128 > 0 ? D * G::kElem / 128 : 1;   // 16-byte chunks per lane and row
-                    constexpr int WORDS = D * G::kElem / 32 / HALVES;                          // words of one: 4, or 2 (e4m3, d = 64)
+                    // ---- outputs: weight 0 times what a masked token holds may be NaN
+                    if constexpr (LDSM) {   // tokens 4 tq .. 4 tq + 3 x d = 16 j + g, + 8
+                        uint32_t keep = 0xffffffffu;
+                        if (partial) {
 #pragma unroll
-                    for (int hf = 0; hf < HALVES; ++hf) {
-                        uint32_t v[4][WORDS];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int n = 2 * tq + (r & 1) + 8 * (r >> 1);
-                            const int dn = (r & 1) + 8 * (r >> 1);
-                            if constexpr (WORDS == 4) {
-                                const uint4 u = lds128(vrow + dn * G::kVec + 16 * cache_chunk(g + 8 * hf, n, G::kChunks));
-                                v[r][0] = u.x, v[r][1] = u.y, v[r][2] = u.z, v[r][3] = u.w;
-                            } else {
-                                const uint2 u = *reinterpret_cast<const uint2 *>(
-                                    buf + G::kBlock + n * G::kVec + 16 * cache_chunk(g / 2, n, G::kChunks) + 8 * (g & 1));
-                                v[r][0] = u.x, v[r][1] = u.y;
-                            }
-                            if (partial && (t0 + n < lo || t0 + n >= hi)) {   // weight 0 times what is there may be NaN
-#pragma unroll
-                                for (int w = 0; w < WORDS; ++w) v[r][w] = 0;
-                            }
+                            for (int e = 0; e < 4; ++e)
+                                if (t0 + 4 * tq + e < lo || t0 + 4 * tq + e >= hi) keep &= ~(0xffu << 8 * e);
                         }
+                        const int n = lane & 15;
 #pragma unroll
-                        for (int w = 0; w < WORDS; ++w) {
-                            if constexpr (E4M3) {
-                                const uint32_t lo01 = __byte_perm(v[0][w], v[1][w], 0x5140);
-                                const uint32_t lo23 = __byte_perm(v[2][w], v[3][w], 0x5140);
-                                const uint32_t hi01 = __byte_perm(v[0][w], v[1][w], 0x7362);
-                                const uint32_t hi23 = __byte_perm(v[2][w], v[3][w], 0x7362);
-                                const uint32_t a0 = cvt_lo(lo01), a1 = cvt_hi(lo01), a2 = cvt_lo(lo23), a3 = cvt_hi(lo23);
-                                const uint32_t b0 = cvt_lo(hi01), b1 = cvt_hi(hi01), b2 = cvt_lo(hi23), b3 = cvt_hi(hi23);
+                        for (int j = 0; j < MT; j += 2) {
+                            uint32_t v[4];
+                            ldsm_t8(v, base + G::kBlock + n * G::kVec + 16 * cache_chunk(j + (lane >> 4), n, G::kChunks));
+                            if (partial) {
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    mma_f16(o[nt][2 * w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-                                    mma_f16(o[nt][2 * w + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+                                for (int e = 0; e < 4; ++e) v[e] &= keep;
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                mma_f16(o[0][j + h], cvt_lo(v[2 * h]), cvt_lo(v[2 * h + 1]), cvt_hi(v[2 * h]), cvt_hi(v[2 * h + 1]), pb[0][0], pb[0][1]);
+                        }
+                    } else {   // tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 x this lane's d
+                        const uint32_t vrow = base + G::kBlock + 2 * tq * G::kVec;
+                        constexpr int HALVES = D * G::kElem / 128 > 0 ? D * G::kElem / 128 : 1;   // 16-byte chunks per lane and row
+                        constexpr int WORDS = D * G::kElem / 32 / HALVES;                          // words of one: 4, or 2 (e4m3, d = 64)
+#pragma unroll
+                        for (int hf = 0; hf < HALVES; ++hf) {
+                            uint32_t v[4][WORDS];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const int n = 2 * tq + (r & 1) + 8 * (r >> 1);
+                                const int dn = (r & 1) + 8 * (r >> 1);
+                                if constexpr (WORDS == 4) {
+                                    const uint4 u = lds128(vrow + dn * G::kVec + 16 * cache_chunk(g + 8 * hf, n, G::kChunks));
+                                    v[r][0] = u.x, v[r][1] = u.y, v[r][2] = u.z, v[r][3] = u.w;
+                                } else {
+                                    const uint2 u = *reinterpret_cast<const uint2 *>(
+                                        buf + G::kBlock + n * G::kVec + 16 * cache_chunk(g / 2, n, G::kChunks) + 8 * (g & 1));
+                                    v[r][0] = u.x, v[r][1] = u.y;
                                 }
-                            } else {
-                                const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
-                                const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
-                                const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
-                                const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+                                if (partial && (t0 + n < lo || t0 + n >= hi)) {
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma_bf16(o[nt][WORDS * hf + w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                                    for (int w = 0; w < WORDS; ++w) v[r][w] = 0;
+                                }
+                            }
+#pragma unroll
+                            for (int w = 0; w < WORDS; ++w) {
+                                if constexpr (E4M3) {
+                                    const uint32_t lo01 = __byte_perm(v[0][w], v[1][w], 0x5140);
+                                    const uint32_t lo23 = __byte_perm(v[2][w], v[3][w], 0x5140);
+                                    const uint32_t hi01 = __byte_perm(v[0][w], v[1][w], 0x7362);
+                                    const uint32_t hi23 = __byte_perm(v[2][w], v[3][w], 0x7362);
+                                    const uint32_t a0 = cvt_lo(lo01), a1 = cvt_hi(lo01), a2 = cvt_lo(lo23), a3 = cvt_hi(lo23);
+                                    const uint32_t b0 = cvt_lo(hi01), b1 = cvt_hi(hi01), b2 = cvt_lo(hi23), b3 = cvt_hi(hi23);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        mma_f16(o[nt][2 * w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                                        mma_f16(o[nt][2 * w + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+                                    }
+                                } else {
+                                    const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
+                                    const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+                                    const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
+                                    const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        mma_bf16(o[nt][WORDS * hf + w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                                }
                             }
                         }
                     }
@@ -601,19 +637,21 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
             for (int i = tid; i < 8 * TURN * (D / 4); i += THREADS) {
                 const int rt = i / (D / 4), r8 = rt % 8, r = 8 * nt + rt, d0 = (i % (D / 4)) * 4;
                 if (r >= rows) break;
-                // where d0 .. d0 + 3 lie: lane group g, tiles j and j + 1, elements c and c + 2
-                int gd, j;
-                if constexpr (!E4M3 && D == 128) gd = d0 % 64 / 8, j = 4 * (d0 / 64) + d0 % 8 / 2;
+                // where d0 .. d0 + 3 lie: lane group gd, tile j, element c, and how far apart in tiles, elements or groups
+                int gd, j, c = r8 & 1;
+                if constexpr (LDSM) gd = d0 % 8, j = d0 / 16, c += d0 % 16 / 8 * 2;
+                else if constexpr (!E4M3 && D == 128) gd = d0 % 64 / 8, j = 4 * (d0 / 64) + d0 % 8 / 2;
                 else gd = d0 / (D / 8), j = d0 % (D / 8) / 2;
-                const float *src = sm.o + rt / 8 * TILE + ((r8 & 1) * MT + j) * Sm::kMerge + 4 * gd + r8 / 2;
+                constexpr int D1 = LDSM ? 4 : 2 * MT * Sm::kMerge, D2 = LDSM ? 8 : Sm::kMerge;
+                const float *src = sm.o + rt / 8 * TILE + (c * MT + j) * Sm::kMerge + 4 * gd + r8 / 2;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
                 for (int w = 0; w < act; ++w, src += 4 * MT * Sm::kMerge) {
                     const float f = sm.m[w][r];
                     x.x = fmaf(f, src[0], x.x);
-                    x.y = fmaf(f, src[2 * MT * Sm::kMerge], x.y);
-                    x.z = fmaf(f, src[Sm::kMerge], x.z);
-                    x.w = fmaf(f, src[(2 * MT + 1) * Sm::kMerge], x.w);
+                    x.y = fmaf(f, src[D1], x.y);
+                    x.z = fmaf(f, src[D2], x.z);
+                    x.w = fmaf(f, src[D1 + D2], x.w);
                 }
                 if (pc.np == 1) {
                     paged_write<__nv_bfloat16, D>(a, pc.b, pc.h, row0 + r, d0, x, sm.part[r]);
