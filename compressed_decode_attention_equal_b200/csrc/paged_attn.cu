@@ -35,8 +35,8 @@ struct MmaSmem {
     using G = CacheGeom<__nv_bfloat16, E4M3, D>;
     static constexpr int kStage = (TP * G::kGroup + 127) / 128 * 128;
     static constexpr int kRows = 8 * NT;
-    // rounds that a unit's query load and outputs take as long as: 1, 2, 3 measured 89.8, 77.5, 80.3 us with one row
-    // (64 ragged sequences x 16 heads), and 1, 2, 3, 4 with 28 rows 58.6, 49.6, 50.2, 49.3 us (48 x 4 heads)
+    // rounds that a unit's query load and outputs take as long as: 1, 2, 3 measured 90.3, 72.4, 73.3 us with one row
+    // (64 ragged sequences x 16 heads), and 1, 2, 3, 4 with 28 rows 58.4, 48.8, 49.8, 47.7 us (48 x 4 heads)
     static constexpr int kCost = NT == 1 ? 2 : 4;
     static constexpr int kQRow = 2 * D + 8;      // bytes of a query row: 8 more than 2 D against bank conflicts
     static constexpr int kMerge = 33;            // words per accumulator element of a warp's 32 lanes
@@ -223,9 +223,9 @@ struct GroupRing {
 //   Weights are rounded to the matrix type (fp16 2^-11, bf16 2^-8 relative): the second product runs on
 //   16-bit operands, and the partition keeps the fp32 weights. Sums and maxima are fp32. A reference maximum
 //   moves only when it is exceeded by 8 (2^8), so that the rescale of O runs rarely.
-// Measured: 32 sequences x 4 heads x 32,768 e4m3 keys at 7 rows take 172 us, 97% of the copy rate (raw, ragged:
+// Measured: 32 sequences x 4 heads x 32,768 e4m3 keys at 7 rows take 174 us, 96% of the copy rate (raw, ragged:
 // 79.5 us, 94%). An mma.sync, a conversion and an FMA add up on one scheduler here instead of overlapping, so
-// that many rows are bound by the instruction rate: 28 rows over 8 x 4 x 16,384 e4m3 keys take 66 us, 32%.
+// that many rows are bound by the instruction rate: 28 rows over 8 x 4 x 16,384 e4m3 keys take 62.5 us, 34%.
 template <bool E4M3, int D, int NT, int W, int S, int CTAS, int TP>
 __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
     using Sm = MmaSmem<E4M3, D, NT, W, S, CTAS, TP>;
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
             const int d0 = E4M3 ? 64 * (ks / 4) + 16 * tq + 4 * (ks % 4) : 32 * (ks / 2) + 8 * tq + 4 * (ks % 2);
             return *reinterpret_cast<const uint2 *>(sm.q[8 * nt + g] + 2 * d0);
         };
-        constexpr bool QREG = NT <= 2;   // the queries stay in registers (16 rows: 46.5 -> 45.0 us; 28 would spill)
+        constexpr bool QREG = NT <= 2;   // the queries stay in registers (16 rows: 43.1 -> 41.1 us; 28 would spill)
         uint2 qf[QREG ? NT : 1][QREG ? KS : 1];
         if constexpr (QREG) {
 #pragma unroll
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
 // keeping one token; for the outputs it takes d / 32 dimensions of all 8 rows (one load of its values per
 // token and the 8 weights broadcast). Raw caches at d = 128 are 16 KB per group, 712 clocks of one SM at the copy
 // rate; its ~350 shared-memory wavefronts and ~1,700 issue slots of one scheduler lie below that, but
-// 8 warps do not hide a group's latency: 8 sequences x 4 heads x 8,192 keys take 64 us, 65% of the copy rate
+// 8 warps do not hide a group's latency: 8 sequences x 4 heads x 8,192 keys take 63.5 us, 65% of the copy rate
 // (88 us with two tokens x two rows per lane).
 constexpr int kF32Rows = 8;
 
@@ -1009,12 +1009,12 @@ cudaError_t launch_mma(const PagedArgs &a, cudaStream_t s) {
 template <bool E4M3, int D>
 cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     // at d = 64 two groups make a tile, which halves what a tile costs beside its products: 32 x 8 heads x 8,192 keys
-    // 74.0 -> 65.5 us (e4m3), 94.1 -> 87.1 us (raw)
+    // 58.9 -> 55.0 us (e4m3), 89.6 -> 86.4 us (raw)
     constexpr int TP = D == 64 ? 2 : 1;
-    // Warps and CTAs per SM. e4m3, 8 rows: two CTAs of 8 warps at 128 registers (7B batch 172 us; one CTA of 8 warps
-    // 223 us: too few to hide a tile's latency). Raw tiles are twice the bytes for the same work: one CTA of 8
-    // warps (79.3 us; two of 4 84.7). More rows need the registers: 16 and 28 rows 45.0 and 65.9 us; with three
-    // and two CTAs of 4 warps 49.3 and 75.5.
+    // Warps and CTAs per SM. e4m3, 8 rows: two CTAs of 8 warps at 128 registers (7B batch 174 us; one CTA of 8 warps
+    // 188 us: too few to hide a tile's latency). Raw tiles are twice the bytes for the same work: one CTA of 8
+    // warps (79.4 us; two of 4 84.2). More rows need the registers: 16 and 28 rows 41.1 and 62.5 us; with three
+    // and two CTAs of 4 warps 55.8 and 75.2.
     if constexpr (E4M3) {
         if (a.pass_rows == 8) return launch_mma<E4M3, D, 1, 8, 2, 2, TP>(a, s);
         if (a.pass_rows == 16) return launch_mma<E4M3, D, 2, 8, 3, 1, TP>(a, s);
