@@ -11,7 +11,8 @@ namespace {
 constexpr size_t kTicketOffset = 64;   // the append's CTA count, inside the workspace header
 // The attention's counters have a place of their own for the most units of any call, so that calls of
 // different shapes can share a workspace: no call's partials lie where another's counters are.
-constexpr size_t kPartOffset = kWsHeader + static_cast<size_t>(kMaxPagedUnits) * 4;
+constexpr size_t kPartOffset = kWsHeader + (static_cast<size_t>(kMaxPagedUnits) + 2 * kMaxPagedCtas) * 4;
+static_assert(kPartOffset % 256 == 0, "partials start on 256 bytes");
 constexpr int64_t kMaxCacheTokens = int64_t{1} << 30;   // per sequence: positions are int32
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

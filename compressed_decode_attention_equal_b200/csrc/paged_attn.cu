@@ -40,10 +40,10 @@ struct MmaSmem {
     static constexpr int kCost = NT == 1 ? 2 : 4;
     static constexpr int kQRow = 2 * D + 8;      // bytes of a query row: 8 more than 2 D against bank conflicts
     static constexpr int kMerge = 33;            // words per accumulator element of a warp's 32 lanes
-    static constexpr int kMaxCtas = CTAS * 160;  // the join of a unit's pieces keeps a word per row and piece in o
+    static constexpr int kMaxCtas = CTAS * 160;
     static constexpr int kTurn = NT < 2 ? NT : 2;   // tiles of 8 rows that the warps join at once
     static constexpr int kOut = kTurn * W * 4 * (D / 16) * kMerge;
-    static constexpr int kJoin = kRows * (kMaxCtas + 1);
+    static constexpr int kJoin = kRows * 33;     // the join of a unit's pieces keeps their weights in o
     alignas(128) uint8_t ring[W][S][kStage];
     float o[kOut > kJoin ? kOut : kJoin];        // kTurn tiles of all warps: [kTurn][W][4 D / 16][kMerge]
     alignas(16) uint8_t q[kRows][kQRow];
@@ -685,9 +685,9 @@ template <bool E4M3, int D, int W, int S>
 struct F32Smem {
     using G = CacheGeom<float, E4M3, D>;
     static constexpr int kStage = (G::kGroup + 127) / 128 * 128;
-    static constexpr int kMaxCtas = 160;             // the join of a unit's pieces keeps a word per row and piece in o
+    static constexpr int kMaxCtas = 160;
     static constexpr int kCost = 2;
-    static constexpr int kOut = W * kF32Rows * D, kJoin = kF32Rows * (kMaxCtas + 1);
+    static constexpr int kOut = W * kF32Rows * D, kJoin = kF32Rows * 33;   // kJoin: the weights of a unit's pieces
     alignas(128) uint8_t ring[W][S][kStage];
     alignas(16) float o[kOut > kJoin ? kOut : kJoin];   // [W][rows][D]
     alignas(16) float q[kF32Rows][D + 4];

@@ -254,7 +254,7 @@ struct PagedArgs {
     int ncta;
     float *part_o;                       // [ncta][2][pass_rows][d] split partial outputs (normalised)
     float *part_l;                       // [ncta][2][pass_rows] their log2 partitions
-    int32_t *counters;                   // [units] pieces done (zero between calls)
+    int32_t *counters;                   // pieces done: [kMaxPagedUnits], then by group of pieces [2 kMaxPagedCtas] (zero between calls)
     uint32_t *flags;
 };
 

@@ -88,13 +88,15 @@ struct ChunkValues {
 // ---------------------------------------------------------------------------
 constexpr int kPieceTable = 32;   // pieces of a CTA's range that are laid out at once
 
+// Place of a partial: a unit's pieces but the first start their CTA's range, its first ends it.
+__device__ __forceinline__ int64_t paged_slot(int c0, int k) { return 2 * static_cast<int64_t>(c0 + k) + (k == 0 ? 1 : 0); }
+
 struct PagedPiece {
     int b, h, pass;
     int r0, r1, rounds;   // rounds [r0, r1) of the unit's; r1 = r0: the range cuts only the unit's fixed weight
     int lo, hi;           // the sequence's keys
     int c0, np;           // CTA of the unit's first piece, pieces (1: this one is the whole unit)
-    // a unit's pieces but the first start their CTA's range, its first ends it
-    __device__ __forceinline__ int64_t slot(int cta) const { return 2 * static_cast<int64_t>(cta) + (r0 == 0 ? 1 : 0); }
+    __device__ __forceinline__ int64_t slot(int cta) const { return paged_slot(c0, cta - c0); }
 };
 
 struct PagedSched {
@@ -169,17 +171,16 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs &a, PagedSched &s
 
 // Lay out pieces `from` .. `from` + 31 of this CTA's range (all threads; ends with a barrier; the caller
 // puts one in front where the table is still in use). One lane per unit. With too little work fewer CTAs
-// get a range: a unit's pieces are joined by one CTA, at a cost for each. A kernel runs this code once or
+// get a range. A kernel runs this code once or
 // twice, so that it is kept short: instruction fetches, not arithmetic, are its time.
 template <int W, int TT, int COST>
 __device__ __forceinline__ void paged_pieces(const PagedArgs &a, PagedSched &s, int from) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x, mult = a.Hkv * a.passes;
         const long long total = s.cum[a.B];
-        // least weight per CTA: 1 or 2 measured 8.9 and 9.6 us (one sequence of 300 tokens, 8 heads), 15.6 and 13.9 us
-        // (one of 10,500, 2 heads: 82 pieces a unit or 41)
-        const int least = total <= 16ll * a.B * mult ? 1 : 2;
-        const int ctas = static_cast<int>(min(static_cast<long long>(a.ncta), max(1ll, total / least)));
+        // as many ranges as there is weight for: with a least weight of 2 one sequence of 10,500 tokens and 2 heads (82
+        // pieces a unit, or 41) takes 13.8 us, not 13.3
+        const int ctas = static_cast<int>(min(static_cast<long long>(a.ncta), max(1ll, total)));
         // lanes 0 and 1: this CTA's range
         const int c = blockIdx.x + (lane & 1);
         const long long edge = c <= ctas ? total * c / ctas : total;
@@ -271,52 +272,45 @@ __device__ __forceinline__ void paged_write(const PagedArgs &a, int b, int h, in
     if (d0 == 0) a.lse[r] = l2 * 0.69314718055994530942f;
 }
 
-// Join the pieces of one unit and write its outputs. All threads of the CTA. First the pieces' weights,
-// 2^(l - largest l) over their sum, into `scratch` (rows x (pieces + 1) words, one warp per row and one
-// round trip for 32 pieces); then each thread sums four outputs of a row over the pieces, AHEAD loads in
-// flight. The order of the sum is that of the pieces, whichever CTA this is.
+constexpr int kJoinAhead = 8;    // partial outputs that a joining thread has in flight
+constexpr int kJoinWhole = 24;   // a unit's pieces that one CTA joins
+constexpr int kJoinGroup = 8;    // more are joined in groups of 8, or larger ones from 256 pieces on
+static_assert(kMaxPagedCtas <= 32 * 32 && kJoinWhole <= 32, "at most 32 pieces or groups are joined at once");
+
+// Join the np <= 32 pieces k0, k0 + step, ... of one unit, into its outputs (`whole`) or into the first one's
+// partial. All threads of the CTA. First the pieces' weights, 2^(l - largest l) over their sum, into `scratch` (33
+// words per row; a warp per row, a lane per piece); then each thread sums four outputs of a row over the
+// pieces, kJoinAhead loads in flight. The order of the sum is that of the pieces.
 template <typename T, int D, int PASS, int THREADS>
-__device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedPiece &p, float *scratch) {
-    constexpr int AHEAD = 8;
-    const int lane = threadIdx.x & 31, c0 = p.c0, np = p.np, row0 = p.pass * PASS;
+__device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedPiece &p, float *scratch, int k0, int step, int np, bool whole) {
+    constexpr int AHEAD = kJoinAhead, WARPS = THREADS / 32, RPW = (PASS + WARPS - 1) / WARPS;   // rows per warp, together
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = p.c0, row0 = p.pass * PASS;
     const int rows = min(PASS, a.rows - row0);
-    const auto slot = [&](int k, int row) { return (2 * static_cast<int64_t>(c0 + k) + (k == 0 ? 1 : 0)) * PASS + row; };
-    float *parts = scratch + rows * np;   // the rows' log2 partitions
-    constexpr int WARPS = THREADS / 32, RPW = (PASS + WARPS - 1) / WARPS;   // rows per warp, loaded together
-    const int warp = threadIdx.x >> 5;
-    float first[RPW];
+    const auto slot = [&](int k, int row) { return paged_slot(c0, k0 + k * step) * PASS + row; };
+    float l[RPW];
 #pragma unroll
     for (int i = 0; i < RPW; ++i)
-        first[i] = warp + i * WARPS < rows && lane < np ? __ldcg(a.part_l + slot(lane, warp + i * WARPS)) : -INFINITY;
+        l[i] = warp + i * WARPS < rows && lane < np ? __ldcg(a.part_l + slot(lane, warp + i * WARPS)) : -INFINITY;
+    const auto across = [](float x, auto op) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+        return x;
+    };
 #pragma unroll
     for (int i = 0; i < RPW; ++i) {
-        const int row = warp + i * WARPS;
-        if (row >= rows) break;
-        float *wt = scratch + row * np;
-        float top = first[i], sum = 0.f;
-        if (lane < np) wt[lane] = first[i];
-#pragma unroll 1
-        for (int k = lane + 32; k < np; k += 32) {
-            wt[k] = __ldcg(a.part_l + slot(k, row));
-            top = fmaxf(top, wt[k]);
-        }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        float top = across(l[i], [](float x, float y) { return fmaxf(x, y); });
         top = top > -INFINITY ? top : 0.f;   // no piece with a key: every weight is 2^-inf = 0
-#pragma unroll 1
-        for (int k = lane; k < np; k += 32) sum += wt[k] = ex2(wt[k] - top);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);
-#pragma unroll 1
-        for (int k = lane; k < np; k += 32) wt[k] *= inv;
-        if (lane == 0) parts[row] = sum == 0.f ? -INFINITY : top + __log2f(sum);
+        const float w = ex2(l[i] - top), sum = across(w, [](float x, float y) { return x + y; });
+        if (warp + i * WARPS < rows) {
+            scratch[33 * (warp + i * WARPS) + lane] = sum == 0.f ? 0.f : w * __frcp_rn(sum);
+            if (lane == 0) scratch[33 * (warp + i * WARPS) + 32] = sum == 0.f ? -INFINITY : top + __log2f(sum);   // the row's log2 partition
+        }
     }
     __syncthreads();
 #pragma unroll 1
     for (int i = threadIdx.x; i < rows * (D / 4); i += THREADS) {
         const int row = i / (D / 4), d0 = (i % (D / 4)) * 4;
-        const float *wt = scratch + row * np;
+        const float *wt = scratch + 33 * row;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
         for (int k = 0; k < np; k += AHEAD) {
@@ -326,31 +320,50 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedPiece 
                 v[e] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot(min(k + e, np - 1), row) * D + d0));
 #pragma unroll
             for (int e = 0; e < AHEAD; ++e) {
-                const float f = k + e < np ? wt[k + e] : 0.f;
+                const float f = wt[k + e];   // 0 behind the last piece
                 o = make_float4(fmaf(f, v[e].x, o.x), fmaf(f, v[e].y, o.y), fmaf(f, v[e].z, o.z), fmaf(f, v[e].w, o.w));
             }
         }
-        paged_write<T, D>(a, p.b, p.h, row0 + row, d0, o, parts[row]);
+        if (whole) {
+            paged_write<T, D>(a, p.b, p.h, row0 + row, d0, o, wt[32]);
+        } else {   // read before by this thread alone, the partitions before the barrier
+            store4(a.part_o + slot(0, row) * D + d0, o);
+            if (d0 == 0) a.part_l[slot(0, row)] = wt[32];
+        }
     }
 }
 
-// Count this CTA's piece of the unit; the CTA that counts the last one joins them. All threads
+// Count this CTA's piece of the unit; the CTA that counts the last one joins them, whichever it is in the same
+// order. More than kJoinWhole pieces are joined in two steps, each group of neighbours by the CTA that counts its
+// last, so that no CTA walks along many pieces: 37 pieces of 28 rows (one sequence of 32,768 tokens, 4 heads) 37.5
+// -> 33.5 us; the second step costs about 2 us, so that 20 pieces take 21.0 us in one and 22.9 in two. All threads
 // of the CTA, after its partial is written.
 template <typename T, int D, int PASS, int THREADS>
 __device__ __forceinline__ void paged_finish_piece(const PagedArgs &a, const PagedPiece &p, PagedSched &s, float *scratch) {
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int *counter = a.counters + (static_cast<int64_t>(p.b) * a.Hkv + p.h) * a.passes + p.pass;
-        const bool last = atomicAdd(counter, 1) == p.np - 1;
-        if (last) *counter = 0;   // ready for the next call
-        s.last = last;
+    int *unit = a.counters + (static_cast<int64_t>(p.b) * a.Hkv + p.h) * a.passes + p.pass;
+    const int group = max(kJoinGroup, (p.np + 31) / 32);
+    bool whole = p.np <= kJoinWhole;
+    int k0 = whole ? 0 : (static_cast<int>(blockIdx.x) - p.c0) / group * group, step = 1;
+    int n = whole ? p.np : min(group, p.np - k0);
+#pragma unroll 1
+    while (true) {
         __threadfence();
-    }
-    __syncthreads();
-    if (s.last) {
-        paged_join<T, D, PASS, THREADS>(a, p, scratch);
         __syncthreads();
+        if (threadIdx.x == 0) {
+            int *counter = whole ? unit : a.counters + kMaxPagedUnits + paged_slot(p.c0, k0);
+            const bool last = atomicAdd(counter, 1) == n - 1;
+            if (last) *counter = 0;   // ready for the next call
+            s.last = last;
+            __threadfence();
+        }
+        __syncthreads();
+        if (!s.last) return;
+        paged_join<T, D, PASS, THREADS>(a, p, scratch, k0, step, n, whole);
+        __syncthreads();
+        if (whole) return;
+        whole = true;
+        k0 = 0, step = group;
+        n = (p.np + group - 1) / group;
     }
 }
 
