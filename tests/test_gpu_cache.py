@@ -395,6 +395,28 @@ def test_attention_many_long_units(dtype, fmt, d, G):
     check_shared(out, lse, q, k.view(Hkv, T, d).double(), v.view(Hkv, T, d).double(), lens, dtype, fmt)
 
 
+@pytest.mark.parametrize("dtype,fmt,d", [(BF, "e4m3", 128), (BF, "raw", 64), (F32, "e4m3", 64)])
+@pytest.mark.parametrize("B,Hkv,G", [(1, 1, 7), (1, 2, 28), (1, 5, 1), (2, 3, 4), (3, 3, 12)])
+def test_attention_few_long_units(dtype, fmt, d, B, Hkv, G):
+    """Units of tens to hundreds of pieces, joined in one step or two; a second call on the same workspace finds its
+    counters as the first did."""
+    T = 50000
+    lens = [T - 7777 * b for b in range(B)]
+    cache, table = make(1, Hkv, d, dtype, fmt, [T], seed=4)
+    g = torch.Generator(device="cuda").manual_seed(d + G)
+    k, v = (torch.randn(T, Hkv, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    skv.cache_append(k, v, cache, table, i32([0]))
+    k, v = skv.cache_read(cache, table, [0], [T])
+    q = torch.randn(B, 1, G * Hkv, d, generator=g, device="cuda").to(dtype)
+    table = table.expand(B, -1).contiguous()
+    ws = torch.zeros(skv.paged_attn_workspace_bytes(B, 1, G * Hkv, Hkv, d, table.shape[1]), dtype=torch.uint8, device="cuda")
+    out, lse = skv.paged_attn(q, cache, table, i32(lens), workspace=ws)
+    ok(ws)
+    check_shared(out, lse, q, k.view(Hkv, T, d).double(), v.view(Hkv, T, d).double(), lens, dtype, fmt)
+    again, lse2 = skv.paged_attn(q, cache, table, i32(lens), workspace=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "raw"])
 def test_attention_peaked_and_unequal_scales(fmt):
     """One key far above the others, values of very unequal size, equal keys: the running maximum and the value
