@@ -15,6 +15,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kSlack = 8.f;                  // 2^8 times a value's scale, 2^119 at most, stays within fp32
 constexpr float kSpan = 126.f;                 // 2^126 stays finite, and 2^-126 is the smallest normal output
+constexpr float kLeast = 1.17549435e-38f;      // 2^-126, the smallest normal number
 constexpr float kNoLogit = -3.402823466e38f;   // no maximum yet: finite, so that a masked logit (-inf) less it is not NaN
 
 // cap tanh(t) in front of 16-bit products: tanh t = 1 - 2 / (e^(2t) + 1), whose absolute error stays within a few
@@ -220,8 +221,11 @@ struct GroupRing {
 //   scale multiplies the logit, and the value's the weight: the fp16 weight is 2^(s + ve - mw), with mw the
 //   running maximum of base-2 logit + value exponent, beside m, the logits' own, for the partition sum 2^(s - m).
 //   So neither a value's scale nor a value of zeros can take precision from the partition or the other values.
-//   Weights are rounded to the matrix type (fp16 2^-11, bf16 2^-8 relative): the second product runs on
-//   16-bit operands, and the partition keeps the fp32 weights. Sums and maxima are fp32. A reference maximum
+//   Weights are 16-bit operands of the second product, the partition keeps them in fp32. e4m3 caches: one fp16 number
+//   (2^-11 relative), far below what the codes themselves hold. Raw caches hold values whole, so that a weight of one
+//   bf16 number (2^-8) would be their largest error: it is two, its upper half and the rest (2^-16), for twice the second
+//   product's instructions (up to 16 rows in the shadow of the copies: 79.9 and 51.9 us with one or two; 28 rows over
+//   8 x 4 x 16,384 keys 63.6 -> 70.3 us). Sums and maxima are fp32. A reference maximum
 //   moves only when it is exceeded by 8 (2^8), so that the rescale of O runs rarely.
 // Measured: 32 sequences x 4 heads x 32,768 e4m3 keys at 7 rows take 174 us, 96% of the copy rate (raw, ragged:
 // 79.5 us, 94%). An mma.sync, a conversion and an FMA add up on one scheduler here instead of overlapping, so
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                                 for (int j = 0; j < MT; ++j) o[nt][j][c] *= f, o[nt][j][c + 2] *= f;
                             }
                     }
-                    uint32_t pb[NT][2];
+                    uint32_t pb[NT][2], pr[E4M3 ? 1 : NT][2];   // raw: a weight is pb + pr
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float p[4];
@@ -507,8 +511,18 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                             l[nt][c & 1] += p[c];
                             if constexpr (E4M3) p[c] = p[c] * vs[c >> 1] * rw[c & 1];   // in this order within fp32's range
                         }
-                        pb[nt][0] = movmatrix_t(E4M3 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
-                        pb[nt][1] = movmatrix_t(E4M3 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float x = p[2 * c], y = p[2 * c + 1];
+                            if constexpr (E4M3) {
+                                pb[nt][c] = movmatrix_t(pack_f16x2(x, y));
+                            } else {   // upper halves, and what they leave (never 0: an infinite value stays one)
+                                const uint32_t u = __float_as_uint(x), w = __float_as_uint(y);
+                                pb[nt][c] = movmatrix_t(__byte_perm(u, w, 0x7632));
+                                pr[nt][c] = movmatrix_t(pack_bf16x2(fmaxf(x - __uint_as_float(u & 0xffff0000u), kLeast),
+                                                                    fmaxf(y - __uint_as_float(w & 0xffff0000u), kLeast)));
+                            }
+                        }
                     }
                     // ---- outputs: weight 0 times what a masked token holds may be NaN
                     if constexpr (LDSM) {   // tokens 4 tq .. 4 tq + 3 x d = 16 j + g, + 8
@@ -555,9 +569,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                                     for (int w = 0; w < WORDS; ++w) v[r][w] = 0;
                                 }
                             }
+                            if constexpr (E4M3) {
 #pragma unroll
-                            for (int w = 0; w < WORDS; ++w) {
-                                if constexpr (E4M3) {
+                                for (int w = 0; w < WORDS; ++w) {
                                     const uint32_t lo01 = __byte_perm(v[0][w], v[1][w], 0x5140);
                                     const uint32_t lo23 = __byte_perm(v[2][w], v[3][w], 0x5140);
                                     const uint32_t hi01 = __byte_perm(v[0][w], v[1][w], 0x7362);
@@ -569,15 +583,23 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                                         mma_f16(o[nt][2 * w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
                                         mma_f16(o[nt][2 * w + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
                                     }
-                                } else {
-                                    const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
-                                    const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
-                                    const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
-                                    const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-                                        mma_bf16(o[nt][WORDS * hf + w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
                                 }
+                            } else {
+                                uint32_t x[WORDS][4];
+#pragma unroll
+                                for (int w = 0; w < WORDS; ++w) {
+                                    x[w][0] = __byte_perm(v[0][w], v[1][w], 0x5410), x[w][1] = __byte_perm(v[0][w], v[1][w], 0x7632);
+                                    x[w][2] = __byte_perm(v[2][w], v[3][w], 0x5410), x[w][3] = __byte_perm(v[2][w], v[3][w], 0x7632);
+                                }
+#pragma unroll
+                                for (int rest = 1; rest >= 0; --rest)   // the small parts first; the two of one sum apart
+#pragma unroll
+                                    for (int w = 0; w < WORDS; ++w)
+#pragma unroll
+                                        for (int nt = 0; nt < NT; ++nt) {
+                                            const auto &b = rest ? pr[nt] : pb[nt];
+                                            mma_bf16(o[nt][WORDS * hf + w], x[w][0], x[w][1], x[w][2], x[w][3], b[0], b[1]);
+                                        }
                             }
                         }
                     }

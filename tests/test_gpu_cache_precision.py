@@ -1,0 +1,58 @@
+"""Paged attention held to bounds in which every rounding is counted one by one: what the products, the weights and
+the output's type can each put into a result, and nothing for what the formula computes exactly."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_reference as ref
+import compressed_decode_attention_equal_b200 as skv
+from test_gpu_cache import BF, F32, i32, make, reference
+
+pytestmark = pytest.mark.gpu
+
+
+def put(k, v, dtype, fmt, B=1):
+    """A cache whose B sequences share the pages of rows k, v [n, Hkv, d]."""
+    n, Hkv, d = k.shape
+    cache, table = make(1, Hkv, d, dtype, fmt, [n])
+    skv.cache_append(k.to(dtype).cuda(), v.to(dtype).cuda(), cache, table, i32([0]))
+    return cache, table.expand(B, -1).contiguous()
+
+
+@pytest.mark.parametrize("d,Hkv,G,R", [(128, 2, 7, 1), (64, 1, 4, 1), (128, 1, 1, 1), (128, 1, 12, 1), (64, 2, 7, 4), (128, 1, 28, 1)])
+def test_weights_of_raw_caches_keep_sixteen_bits(d, Hkv, G, R):
+    """The second product's weights are a bf16 number and the rest as another: 2^-16 of a weight, not bf16's 2^-8. With
+    values of both signs many outputs are far smaller than the sum of their magnitudes, where 2^-8 of a weight shows
+    and the output's own rounding does not. Bound: weights 2^-16, twice the logits' error, fp32 sums 2^-16 of the mass,
+    and half a step of the output."""
+    lens = [2, 3, 17, 40, 64, 100]
+    g = torch.Generator().manual_seed(d + G)
+    k, v = (torch.randn(100, Hkv, d, generator=g) for _ in range(2))
+    cache, table = put(k, v, BF, "raw", len(lens))
+    q = (torch.randn(len(lens), R, G * Hkv, d, generator=g) / 4).bfloat16().cuda()
+    out, _ = skv.paged_attn(q, cache, table, i32(lens))
+    for b in range(len(lens)):
+        r = reference(q, cache, table, lens, b)
+        inner = r.mass * (2.0 ** -16 + 2.0 ** -16 + 2 * r.dlogit[..., None])
+        bound = inner * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(r.out) + 1e-37
+        err = np.abs(out[b].double().cpu().numpy() - r.out)
+        assert np.all(err <= bound), f"len {lens[b]}: {np.max(err / bound):.2f} bounds"
+
+
+@pytest.mark.parametrize("dtype,d,G", [(BF, 128, 7), (BF, 64, 12), (BF, 128, 28), (F32, 64, 2)])
+def test_an_infinite_value_that_is_seen_stays_infinite(dtype, d, G):
+    """Raw caches hold infinities: with a weight above zero they are the output, of either sign; their neighbours in
+    other dimensions and the rows that do not see them stay finite."""
+    n = 77
+    g = torch.Generator().manual_seed(3)
+    k, v = torch.randn(n, 1, d, generator=g) / 4, torch.randn(n, 1, d, generator=g)
+    v[20, 0, 3], v[61, 0, d - 1] = math.inf, -math.inf
+    cache, table = put(k, v, dtype, "raw", 2)
+    q = (torch.randn(2, 1, G, d, generator=g) / 4).to(dtype).cuda()
+    out, lse = skv.paged_attn(q, cache, table, i32([n, n]), first=i32([0, 62]))
+    assert torch.all(out[0, ..., 3] == math.inf) and torch.all(out[0, ..., d - 1] == -math.inf)
+    rest = out.clone()
+    rest[0, ..., 3] = rest[0, ..., d - 1] = 0
+    assert rest.isfinite().all() and lse.isfinite().all()
