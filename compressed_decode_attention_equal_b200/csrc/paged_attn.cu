@@ -14,6 +14,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kSlack = 8.f;                  // 2^8 times a value's scale, 2^119 at most, stays within fp32
+constexpr float kRaise = 7.f;                  // a weight is at most 2^(kSlack + kRaise), half of what fp16 holds
 constexpr float kSpan = 126.f;                 // 2^126 stays finite, and 2^-126 is the smallest normal output
 constexpr float kLeast = 1.17549435e-38f;      // 2^-126, the smallest normal number
 constexpr float kNoLogit = -3.402823466e38f;   // no maximum yet: finite, so that a masked logit (-inf) less it is not NaN
@@ -219,14 +220,15 @@ struct GroupRing {
 //   Values: transposed by byte permutes of neighbouring tokens' words or, up to 8 rows of e4m3, by the load.
 //   e4m3: codes go to fp16 (exact); a query row is scaled by a power of two into fp16's range, exactly; the key's
 //   scale multiplies the logit, and the value's the weight: the fp16 weight is 2^(s + ve - mw), with mw the
-//   running maximum of base-2 logit + value exponent, beside m, the logits' own, for the partition sum 2^(s - m).
+//   running maximum of base-2 logit + value exponent less 7, beside m, the logits' own, for the partition sum 2^(s - m).
 //   So neither a value's scale nor a value of zeros can take precision from the partition or the other values.
 //   Weights are 16-bit operands of the second product, the partition keeps them in fp32. e4m3 caches: one fp16 number
-//   (2^-11 relative), far below what the codes themselves hold. Raw caches hold values whole, so that a weight of one
-//   bf16 number (2^-8) would be their largest error: it is two, its upper half and the rest (2^-16), for twice the second
-//   product's instructions (up to 16 rows in the shadow of the copies: 79.9 and 51.9 us with one or two; 28 rows over
-//   8 x 4 x 16,384 keys 63.6 -> 70.3 us). Sums and maxima are fp32. A reference maximum
-//   moves only when it is exceeded by 8 (2^8), so that the rescale of O runs rarely.
+//   (2^-11 relative), far below what the codes themselves hold; the 7 put the largest near fp16's top, so that its
+//   smallest steps, 2^-24, are 2^-31 of it: 2^19 keys, a warp's most of one sequence, lose 2^-13 by them. Raw caches
+//   hold values whole, so that a weight of one bf16 number (2^-8) would be their largest error: it is two, its upper
+//   half and the rest (2^-16), for twice the second product's instructions (up to 16 rows in the shadow of the copies:
+//   79.9 and 51.9 us with one or two; 28 rows over 8 x 4 x 16,384 keys 63.6 -> 70.3 us). Sums and maxima are fp32. A
+//   reference maximum moves only when it is exceeded by 8 (2^8), so that the rescale of O runs rarely.
 // Measured: 32 sequences x 4 heads x 32,768 e4m3 keys at 7 rows take 174 us, 96% of the copy rate (raw, ragged:
 // 79.5 us, 94%). An mma.sync, a conversion and an FMA add up on one scheduler here instead of overlapping, so
 // that many rows are bound by the instruction rate: 28 rows over 8 x 4 x 16,384 e4m3 keys take 62.5 us, 34%.
@@ -451,12 +453,13 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                     // The reference maxima: of the logits for the partition and, e4m3, of logit + value exponent for the
                     // weights of the outputs. Both move only when one is exceeded by kSlack (or may be: the larger
                     // of a lane's two exponents stands for both).
+                    const float vtop = fmaxf(ve[0], ve[1]) - kRaise;
                     float over = -INFINITY;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const float m = E4M3 ? fminf(mref[nt][c], mw[nt][c] - fmaxf(ve[0], ve[1])) : mref[nt][c];
+                            const float m = E4M3 ? fminf(mref[nt][c], mw[nt][c] - vtop) : mref[nt][c];
                             over = fmaxf(over, fmaxf(s[nt][c], s[nt][c + 2]) - m);
                         }
                     if (__any_sync(0xffffffffu, over > kSlack)) {
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                                 l[nt][c] *= f;
                                 mref[nt][c] = top;
                                 if constexpr (E4M3) {
-                                    topw = fmaxf(fmaxf(topw, mw[nt][c]), top - kSpan);   // zeros only so far: finite
+                                    topw = fmaxf(fmaxf(topw - kRaise, mw[nt][c]), top - kSpan);   // zeros only so far: finite
                                     f = ex2(mw[nt][c] - topw);
                                     mw[nt][c] = topw;
                                 }

@@ -56,3 +56,28 @@ def test_an_infinite_value_that_is_seen_stays_infinite(dtype, d, G):
     rest = out.clone()
     rest[0, ..., 3] = rest[0, ..., d - 1] = 0
     assert rest.isfinite().all() and lse.isfinite().all()
+
+
+@pytest.mark.parametrize("d,G,Hkv,B", [(128, 1, 8, 512), (128, 12, 8, 256), (64, 28, 8, 256)])
+def test_many_small_weights_beside_a_large_one(d, G, Hkv, B):
+    """e4m3 pages, one key 2^26 above 4,095 equal others: each of these weighs less than half of fp16's smallest step
+    beside a weight of 1, and together they are the whole output in the dimensions where the large one's value is zero.
+    (More units than CTAs, so that one warp sees the large key and hundreds of others.) Bound: a weight is off by
+    2^-11 of itself or by 2^-32 of the largest."""
+    n = 4096
+    k, v = torch.zeros(n, Hkv, d), torch.ones(n, Hkv, d)
+    k[0] = 26 * math.log(2) / math.sqrt(d)                  # q of ones: logit 26 ln 2
+    v[0] = 0
+    v[:, :, 0] = 0
+    v[0, :, 0] = 1
+    cache, table = put(k, v, BF, "e4m3", B)
+    q = torch.ones(B, 1, G * Hkv, d, dtype=BF, device="cuda")
+    lens = [n - b % 7 for b in range(B)]
+    out, lse = skv.paged_attn(q, cache, table, i32(lens))
+    for b in (0, 1, B // 2, B - 1):
+        r = reference(q, cache, table, lens, b)
+        inner = r.mass * (2.0 ** -11 + 2.0 ** -16 + 2 * r.dlogit[..., None]) + 2.0 ** -7 * r.tiny
+        bound = inner * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(r.out) + 1e-37
+        err = np.abs(out[b].double().cpu().numpy() - r.out)
+        assert np.all(err <= bound), f"sequence {b}: {np.max(err / bound):.2f} bounds"
+    assert torch.equal(out, out[:, :, :1].expand_as(out))   # equal rows over equal keys
