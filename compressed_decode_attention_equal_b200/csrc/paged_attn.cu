@@ -19,13 +19,23 @@ constexpr float kSpan = 126.f;                 // 2^126 stays finite, and 2^-126
 constexpr float kLeast = 1.17549435e-38f;      // 2^-126, the smallest normal number
 constexpr float kNoLogit = -3.402823466e38f;   // no maximum yet: finite, so that a masked logit (-inf) less it is not NaN
 
-// cap tanh(t) in front of 16-bit products: tanh t = 1 - 2 / (e^(2t) + 1), whose absolute error stays within a few
-// ulps of 1 over the whole range (the hardware tanh's 2^-11 would show in the logits)
-__device__ __forceinline__ float capped(float t, float cap) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(t * (2.0f * kLog2e)) + 1.0f));
-    return fmaf(-2.0f * cap, r, cap);
-}
+// log2(e) c tanh(x / c), relative to itself 2^-20 or better for every c: up to |x / c| = 1/4 x times the series of
+// tanh(u) / u (the next term is 2^-26), so that no difference of numbers near 1 enters a small logit whatever the cap;
+// above it tanh u = 1 - 2 / (e^(2u) + 1), whose absolute error is a few ulps of 1. (The hardware's tanh is 2^-11 off.)
+struct SoftCap {
+    float inv, cap;   // 1 / c and log2(e) c
+    __device__ __forceinline__ explicit SoftCap(float c) : inv(fminf(1.0f / c, 3.402823466e38f)), cap(c * kLog2e) {}
+    __device__ __forceinline__ float near(float x, float u) const {
+        const float w = u * u;
+        const float t = fmaf(w, fmaf(w, fmaf(w, fmaf(w, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.0f);
+        return x * kLog2e * t;
+    }
+    __device__ __forceinline__ float far(float u) const {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(u * (2.0f * kLog2e)) + 1.0f));
+        return fmaf(-2.0f * cap, r, cap);
+    }
+};
 
 // ---------------------------------------------------------------------------
 // bf16 queries: tensor cores
@@ -278,7 +288,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
             }
         }
     };
-    const float cap_l2 = a.softcap * kLog2e;
+    const SoftCap softcap(a.softcap);
     int from = 0, at = paged_next(sm.sched, 0);
     bool fresh = true;   // a new table: nothing is ahead
 #pragma unroll 1
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
 #pragma unroll
             for (int e = 0; e < PER; e += 2) dst[e / 2] = E4M3 ? pack_f16x2(x[e], x[e + 1]) : pack_bf16x2(x[e], x[e + 1]);
             if (lane == 0) {
-                sm.qfac[r] = a.softcap > 0.f ? fac / a.softcap : fac * kLog2e;
+                sm.qfac[r] = a.softcap > 0.f ? fac : fac * kLog2e;
                 sm.slope[r] = qslope[i] * kLog2e;
             }
         }
@@ -433,9 +443,21 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                         }
                     if (a.softcap > 0.f) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float u[4];
+                            bool far = false;
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) s[nt][c] = capped(s[nt][c], cap_l2);
+                            for (int c = 0; c < 4; ++c) {
+                                u[c] = s[nt][c] * softcap.inv;
+                                s[nt][c] = softcap.near(s[nt][c], u[c]);
+                                far |= !(fabsf(u[c]) < 0.25f);
+                            }
+                            if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    if (!(fabsf(u[c]) < 0.25f)) s[nt][c] = softcap.far(u[c]);
+                            }
+                        }
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -847,7 +869,10 @@ __global__ void __launch_bounds__(32 * W, 1) k_paged_f32(const PagedArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     float z = s[r] * ks;
-                    if (a.softcap > 0.f) z = a.softcap * tanhf(z / a.softcap);
+                    if (a.softcap > 0.f) {   // c tanh(z / c); below 2^-12 that is z to the last bit, and z / c may be subnormal
+                        const float t = z / a.softcap;
+                        if (!(fabsf(t) < 0x1p-12f)) z = a.softcap * tanhf(t);
+                    }
                     z = in ? z - sm.slope[4 * rg + r] * gap : -INFINITY;
                     float top = z;
 #pragma unroll

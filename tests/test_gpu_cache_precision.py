@@ -81,3 +81,24 @@ def test_many_small_weights_beside_a_large_one(d, G, Hkv, B):
         err = np.abs(out[b].double().cpu().numpy() - r.out)
         assert np.all(err <= bound), f"sequence {b}: {np.max(err / bound):.2f} bounds"
     assert torch.equal(out, out[:, :, :1].expand_as(out))   # equal rows over equal keys
+
+
+@pytest.mark.parametrize("dtype,fmt", [(BF, "e4m3"), (BF, "raw"), (F32, "e4m3"), (F32, "raw")])
+@pytest.mark.parametrize("cap", [1e-40, 1e-3, 0.5, 6.0, 30.0, 1e3, 1e6, 1e8, 3e38])
+@pytest.mark.parametrize("d,G", [(128, 3), (64, 13), (64, 25)])
+def test_caps_of_every_size(dtype, fmt, cap, d, G):
+    """c tanh(s / c) for any finite c > 0: tiny (the sign of s alone is left), in the range of the logits, and so large
+    that nothing is capped. A capped logit is off by its own product's error and 2^-20 of itself, not of the cap."""
+    n = 211
+    g = torch.Generator().manual_seed(G)
+    k, v = torch.randn(n, 1, d, generator=g) * 2, torch.randn(n, 1, d, generator=g)
+    cache, table = put(k, v, dtype, fmt)
+    q = torch.randn(1, 1, G, d, generator=g).to(dtype).cuda()
+    out, lse = skv.paged_attn(q, cache, table, i32([n]), softcap=cap)
+    (kk, vv), (_, vs) = ref.read_rows(cache, table[0].tolist(), 0, n)
+    cap = float(np.float32(cap))
+    x = q[0].double().cpu().numpy()
+    r = ref.Attn(x, kk, vv, vs, n - 1, 0, softcap=cap)
+    top = np.abs(x[0] @ kk[:, 0].T).max(-1) / math.sqrt(d)
+    r.dlogit = ref.Attn(x, kk, vv, vs, n - 1, 0).dlogit + 2.0 ** -20 * np.minimum(cap, top)
+    ref.check_attention(out[0], lse[0], r, dtype, fmt, f"cap {cap}")
