@@ -1,4 +1,4 @@
-// The exact-token cache's page geometry and the scheduling, joining and output code that its
+// The exact-token cache's launch arguments, page geometry and the scheduling, joining and output code that its
 // attention kernels share.
 //
 // A page holds 64 tokens of one sequence for all its KV heads, [Hkv][4][group]; a group holds 16
@@ -18,6 +18,87 @@
 
 namespace skv {
 
+// ---------------------------------------------------------------------------
+// arguments of the launches (token_cache.cu, paged_attn.cu)
+// ---------------------------------------------------------------------------
+struct AppendArgs {
+    const void *k, *v;                   // [n_tokens][Hkv][d], strides in elements
+    int64_t k_token, k_head, v_token, v_head;
+    int B, Hkv, d, dtype, format;
+    int n_tokens;
+    int per_seq;                         // tokens per sequence when cu is null
+    int per_warp;                        // steps that one warp takes
+    const int32_t *cu;                   // [B + 1] offsets of the sequences' new tokens, or null
+    uint8_t *pages;
+    int64_t num_pages;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *lens;
+    int32_t *new_lens;
+    uint32_t *flags;
+    uint32_t *ticket;                    // CTAs done (zero between calls)
+};
+
+// What cache_read takes of each sequence, passed by value.
+struct ReadRow {
+    int64_t row_off;                     // first output row of the sequence
+    int32_t first, T;                    // positions [first, first + T)
+    int32_t item0;                       // 16-token groups (x heads) of the sequences before it
+    int32_t pad;
+};
+struct ReadTable {
+    ReadRow rows[SKV_MAX_SEQS];
+};
+struct ReadArgs {
+    int B, Hkv, d, dtype, format;
+    int items;                           // groups x heads of all sequences
+    const uint8_t *pages;
+    int64_t num_pages;
+    const int32_t *page_table;
+    int max_pages;
+    void *k, *v;
+    uint32_t *flags;
+};
+
+constexpr int kMaxPagedCtas = 512;       // split partials are sized for this grid
+constexpr int kMaxPagedUnits = 1 << 16;  // (sequence, KV head, pass) units of one call
+
+struct PagedArgs {
+    const void *q;
+    int64_t q_b, q_r, q_h;               // strides in elements
+    const uint8_t *pages;
+    int64_t num_pages;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *lens, *first;         // first may be null
+    int window;                          // 0: no window
+    float scale;                         // logit scale (natural units)
+    float softcap;                       // 0: none
+    const float *slopes;                 // [Hq] or null
+    const void *prior_out;
+    const float *prior_lse;              // null: no prior
+    void *out;
+    float *lse;
+    int B, R, Hq, Hkv, G, d, dtype, format;
+    float inv_G;                         // 1 / G
+    int rows;                            // R * G query rows per KV head
+    int pass_rows, passes;               // rows one pass over the keys serves, ceil(rows / pass_rows)
+    int ncta;
+    float *part_o;                       // [ncta][2][pass_rows][d] split partial outputs (normalised)
+    float *part_l;                       // [ncta][2][pass_rows] their log2 partitions
+    int32_t *counters;                   // pieces done: [kMaxPagedUnits], then by group of pieces [2 kMaxPagedCtas] (zero between calls)
+    uint32_t *flags;
+};
+
+// Rows a pass over the keys serves for this call (paged_attn.cu chooses the kernel by it).
+int paged_pass_rows(int dtype, int rows);
+cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t s);
+cudaError_t launch_cache_read(const ReadArgs &a, const ReadTable &t, cudaStream_t s);
+cudaError_t launch_paged_attn(const PagedArgs &a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// page geometry
+// ---------------------------------------------------------------------------
 constexpr int kGroupTokens = 16;
 constexpr int kPageGroups = SKV_CACHE_PAGE_TOKENS / kGroupTokens;
 constexpr int kScaleExpMin = -100, kScaleExpMax = 119;   // scale exponents of an e4m3 row
