@@ -661,7 +661,10 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
             float sum = f * sm.l[w][r];
 #pragma unroll
             for (int x = 1; x < W; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            sm.m[w][r] = sum == 0.f ? 0.f : (E4M3 ? ex2(sm.mw[E4M3 ? w : 0][r] - top) : f) * __frcp_rn(sum);
+            // 2^7 apart, since ex2 flushes what is below 2^-126; the product may be subnormal
+            const float part = E4M3 ? ex2(sm.mw[E4M3 ? w : 0][r] + kRaise - top) * 0x1p-7f : f;
+            static_assert(kRaise == 7.f, "one factor");
+            sm.m[w][r] = sum == 0.f ? 0.f : part * __frcp_rn(sum);
             if (w == 0) sm.part[r] = sum == 0.f ? -INFINITY : top + __log2f(sum);
         }
         // one copy of this code for all tiles: each turn writes the first kTurn and moves the others down
