@@ -48,17 +48,22 @@ __device__ __forceinline__ void load_row(const T *p, uint32_t (&w)[W]) {   // 4 
     }
 }
 
-// Tokens of sequence b, from its offsets (null: the same number for each); false if they do not
-// run upwards within the n_tokens rows.
-__device__ __forceinline__ bool append_count(const AppendArgs &a, int b, int *count) {
-    if (!a.cu) {
-        *count = a.per_seq;
-        return true;
+// Offsets that do not all run upwards within the n_tokens rows are walked from the first one on: a sequence gets its
+// rows if they run upwards and begin at or behind the end of those that the sequences before it got, so that no row
+// is two sequences' and a length counts what was written. For i >= 0 the sequence that row i went to and i's place
+// there, else `seq` and how many rows it got; b = -1: none.
+struct Walked {
+    int b, n;
+};
+__device__ __noinline__ Walked walk_offsets(const int32_t *cu, int B, int n_tokens, int i, int seq) {
+    int end = 0;
+    for (int b = 0; b < B; ++b) {
+        const int c0 = cu[b], c1 = cu[b + 1];
+        const bool ok = c0 >= end && c1 >= c0 && c1 <= n_tokens;
+        if (i >= 0 ? ok && i >= c0 && i < c1 : b == seq) return {ok ? b : -1, ok ? (i >= 0 ? i : c1) - c0 : 0};
+        if (ok) end = c1;
     }
-    const int c0 = a.cu[b], c1 = a.cu[b + 1];
-    const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.n_tokens;
-    *count = ok ? c1 - c0 : 0;
-    return ok;
+    return {-1, 0};
 }
 
 // the larger of each bf16 pair; of a number and NaN the number
@@ -199,45 +204,53 @@ __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_c
     };
     uint32_t next[kHeads][W] = {};
     load_step(0, next);
+    bool down = false;   // offsets that do not run upwards within the rows
+    if (a.cu)
+        for (int b = threadIdx.x; b <= a.B; b += 32 * kAppendWarps)
+            down |= a.cu[b] < (b > 0 ? a.cu[b - 1] : 0) || a.cu[b] > a.n_tokens;
     // lane t: the group that token (row) t goes to (-1: none; the first head's) and its slot there
-    int where = -1, slot16 = 0;
+    int where = -1, slot16 = 0, i = 0, head = h0;
+    bool bad_page = false;
+    const auto place = [&](int b, int off) {
+        const int len = a.lens[b];
+        const int64_t pos = static_cast<int64_t>(len) + off;
+        if (len < 0 || pos >= static_cast<int64_t>(a.max_pages) * SKV_CACHE_PAGE_TOKENS) return;   // flagged below
+        const int page = a.page_table[static_cast<int64_t>(b) * a.max_pages + pos / SKV_CACHE_PAGE_TOKENS];
+        const int slot = static_cast<int>(pos) % SKV_CACHE_PAGE_TOKENS;
+        slot16 = slot % kGroupTokens;
+        bad_page = page < 0 || page >= a.num_pages;
+        if (!bad_page) where = (page * a.Hkv + head) * kPageGroups + slot / kGroupTokens;   // fits: checked on the host
+    };
     if (lane < count) {
-        const int i = static_cast<int>(FLAT ? (i0 + lane) / a.Hkv : i0 + lane);
-        const int head = FLAT ? static_cast<int>(i0 + lane - static_cast<int64_t>(i) * a.Hkv) : h0;
-        int b, off;
-        bool ok = true;
+        i = static_cast<int>(FLAT ? (i0 + lane) / a.Hkv : i0 + lane);
+        if constexpr (FLAT) head = static_cast<int>(i0 + lane - static_cast<int64_t>(i) * a.Hkv);
         if (a.cu) {
-            int lo = -1, hi = a.B;   // cu[lo] <= i < cu[hi] (cu[-1] = -inf, cu[B] only read below)
+            int lo = -1, hi = a.B;   // cu[lo] <= i < cu[hi] (cu[-1] = -inf)
             while (hi - lo > 1) {
                 const int m = (lo + hi) >> 1;
                 if (a.cu[m] <= i) lo = m;
                 else hi = m;
             }
-            b = lo;
-            int n = 0;
-            ok = b >= 0 && append_count(a, b, &n);
-            off = ok ? i - a.cu[b] : 0;
-            ok = ok && off >= 0 && off < n;   // rows behind the last sequence are no one's
+            if (lo >= 0 && i < a.cu[lo + 1]) place(lo, i - a.cu[lo]);   // rows behind the last sequence are no one's
         } else {
-            b = i / a.per_seq;
-            off = i - b * a.per_seq;
-        }
-        if (ok) {
-            const int len = a.lens[b];
-            const int64_t pos = static_cast<int64_t>(len) + off;
-            if (len >= 0 && pos < static_cast<int64_t>(a.max_pages) * SKV_CACHE_PAGE_TOKENS) {   // else flagged below
-                const int page = a.page_table[static_cast<int64_t>(b) * a.max_pages + pos / SKV_CACHE_PAGE_TOKENS];
-                const int slot = static_cast<int>(pos) % SKV_CACHE_PAGE_TOKENS;
-                slot16 = slot % kGroupTokens;
-                if (page < 0 || page >= a.num_pages) raise_flag(a.flags, FLAG_BAD_PAGE);
-                else where = (page * a.Hkv + head) * kPageGroups + slot / kGroupTokens;   // fits: checked on the host
-            }
+            const int b = i / a.per_seq;
+            place(b, i - b * a.per_seq);
         }
     }
+    const bool walk = __syncthreads_or(down);
+    if (walk) {
+        where = -1;
+        bad_page = false;
+        if (lane < count) {
+            const Walked at = walk_offsets(a.cu, a.B, a.n_tokens, i, 0);
+            if (at.b >= 0) place(at.b, at.n);
+        }
+        __syncthreads();
+    }
+    if (bad_page) raise_flag(a.flags, FLAG_BAD_PAGE);
     // The CTA that comes last to this point writes the new lengths: new_lens may be lens itself, which every
     // CTA has read by then (here and not at the end, so that no warp waits for the others' tokens).
     __shared__ int s_last;
-    __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
         s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
@@ -247,8 +260,15 @@ __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_c
     if (s_last) {
         for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
             const int len = a.lens[b];
-            int n;
-            bool ok = append_count(a, b, &n);
+            int n = a.per_seq;
+            bool ok = true;
+            if (walk) {
+                const Walked got = walk_offsets(a.cu, a.B, a.n_tokens, -1, b);
+                ok = got.b >= 0;
+                n = got.n;
+            } else if (a.cu) {
+                n = a.cu[b + 1] - a.cu[b];
+            }
             const int64_t cap = static_cast<int64_t>(a.max_pages) * SKV_CACHE_PAGE_TOKENS;
             int64_t to = static_cast<int64_t>(len) + n;
             if (len < 0 || len > cap) {

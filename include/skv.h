@@ -443,8 +443,8 @@ size_t skv_cache_page_bytes(skv_dtype dtype, skv_cache_format format, int Hkv, i
  *             call returns to zero.
  * One launch, graph-capturable. Device-detected, the offending tokens skipped: a page id outside the
  * cache; lens below zero or above max_pages * 64 (the sequence is left as it is); tokens behind
- * that capacity (new_lens is then the capacity); a cu_new that does not run upwards within n_tokens
- * (that sequence gets none). Errors: SKV_ERR_INVALID_ARG, SKV_ERR_UNSUPPORTED (dtype, d, more than
+ * that capacity (new_lens is then the capacity); offsets cu_new[b], cu_new[b + 1] that do not run upwards within
+ * n_tokens, or begin before the end of the rows that an earlier sequence got (sequence b gets none). Errors: SKV_ERR_INVALID_ARG, SKV_ERR_UNSUPPORTED (dtype, d, more than
  * INT32_MAX token-heads), SKV_ERR_WORKSPACE, SKV_ERR_CUDA.
  */
 skv_status skv_cache_append(const void *k, const void *v, skv_dtype dtype, int64_t k_token_stride,

@@ -1,0 +1,58 @@
+"""Calls of the exact-token cache that its documentation allows, beyond the ordinary ones: offsets in any order, options
+with every kind of row tile, joins of many rows and passes, and arguments at the ends of their ranges."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_reference as ref
+import compressed_decode_attention_equal_b200 as skv
+from compressed_decode_attention_equal_b200 import _lib
+from test_gpu_cache import BF, F32, filled, i32, make, ok, rand, reference
+
+pytestmark = pytest.mark.gpu
+
+
+def granted(cu, n):
+    """Rows of each sequence by the documented rule: upwards within n, and behind the rows of the sequences before."""
+    end, got = 0, []
+    for c0, c1 in zip(cu, cu[1:]):
+        fine = end <= c0 <= c1 <= n
+        got.append((c0, c1) if fine else None)
+        end = c1 if fine else end
+    return got
+
+
+OFFSETS = [([0, 5, 3, 8], 8), ([0, 5, 3, 6], 6), ([3, 1, 4, 4, 9], 9), ([-2, 3, 5, 7], 7), ([0, 4, 20, 6, 8], 8), ([8, 0, 8], 8),
+           ([2, 2, 2], 5), ([0, 9], 8), ([5, 2, 7, 3, 7, 7, 9], 12), ([0, 3, 6, 1, 6, 6, 11], 11)]
+
+
+@pytest.mark.parametrize("d,Hkv,dtype,fmt", [(128, 4, BF, "e4m3"), (64, 3, F32, "raw"), (128, 1, BF, "raw")])
+@pytest.mark.parametrize("cu,n", OFFSETS + [("random", 400)])
+def test_offsets_in_any_order_never_count_what_was_not_written(d, Hkv, dtype, fmt, cu, n):
+    g = torch.Generator().manual_seed(n)
+    if cu == "random":
+        up = np.sort(np.random.RandomState(1).randint(0, n + 1, 151))
+        up[[20, 77, 78, 140]] = up[[90, 10, 150, 0]]        # a few out of place
+        cu = up.tolist()
+    B = len(cu) - 1
+    got = granted(cu, n)
+    old = [(7 * b) % 70 for b in range(B)]
+    want_lens = [o + (r[1] - r[0] if r else 0) for o, r in zip(old, got)]
+    cache, table = make(B, Hkv, d, dtype, fmt, [o + n for o in old], seed=5)
+    want = skv.TokenCache(cache.num_pages, Hkv, d, dtype, format=fmt, device="cpu", pages=cache.pages.cpu().clone())
+    k, v = rand(g, n, Hkv, d, dtype=dtype), rand(g, n, Hkv, d, dtype=dtype)
+    for b, r in enumerate(got):
+        if r:
+            ref.write_rows(want, table[b].tolist(), old[b], k[r[0]:r[1]].double().numpy(), v[r[0]:r[1]].double().numpy())
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    lens = i32(old)
+    assert skv.cache_append(k.cuda(), v.cuda(), cache, table, lens, cu_new=i32(cu), new_lens=lens, workspace=ws).tolist() == want_lens
+    if None in got:
+        assert skv.workspace_error(ws) == (_lib.SKV_ERR_DEVICE, _lib.FLAG_BAD_LENS)
+    ok(ws)
+    a, w = cache.pages.cpu(), want.pages
+    if fmt == "e4m3":   # -0 and +0 are both right where a value rounds to zero
+        a, w = (torch.where(t == 128, 0, t) for t in (a, w))
+    assert torch.equal(a, w)
