@@ -56,3 +56,46 @@ def test_offsets_in_any_order_never_count_what_was_not_written(d, Hkv, dtype, fm
     if fmt == "e4m3":   # -0 and +0 are both right where a value rounds to zero
         a, w = (torch.where(t == 128, 0, t) for t in (a, w))
     assert torch.equal(a, w)
+
+
+@pytest.mark.parametrize("dtype,fmt", [(BF, "e4m3"), (BF, "raw"), (F32, "raw"), (F32, "e4m3")])
+@pytest.mark.parametrize("d,Hkv,G,R", [(64, 2, 4, 1), (64, 1, 6, 2), (128, 2, 3, 5), (128, 1, 9, 4), (64, 2, 7, 4), (128, 1, 5, 9)])
+@pytest.mark.parametrize("window,softcap,alibi,scale", [(0, 0.0, True, None), (47, 4.0, False, 0.2), (0, 30.0, True, -0.05)])
+def test_options_with_every_row_tile(dtype, fmt, d, Hkv, G, R, window, softcap, alibi, scale):
+    """Window, start, cap, bias and scale with one, two and four tiles of rows and with several passes; starts and ends in
+    both halves of the two groups that are copied at once at d = 64."""
+    lens = [500, 1, 97, 64, 260, 40, 30, 333, 48, 300, 80, 32]
+    first = [123, 0, 97, 63, -4, 1000, 17, 240, 16, 31, 48, 0]
+    B = len(lens)
+    cache, table, g = filled(B, Hkv, d, dtype, fmt, lens, seed=d + window)
+    q = torch.randn(B, R, G * Hkv, d, generator=g).to(dtype).cuda()
+    slopes = torch.exp2(-torch.arange(1, G * Hkv + 1).float() / 2).cuda() if alibi else None
+    ws = torch.zeros(skv.paged_attn_workspace_bytes(B, R, G * Hkv, Hkv, d, table.shape[1]), dtype=torch.uint8, device="cuda")
+    out, lse = skv.paged_attn(q, cache, table, i32(lens), first=i32(first), window=window, softcap=softcap, slopes=slopes,
+                              scale=scale, workspace=ws)
+    ok(ws)
+    sl = None if slopes is None else slopes.double().cpu().numpy()
+    for b in range(B):
+        r = reference(q, cache, table, lens, b, first=first[b], window=window, softcap=softcap, slopes=sl, scale=scale)
+        ref.check_attention(out[b], lse[b], r, dtype, fmt, f"sequence {b}")
+
+
+@pytest.mark.parametrize("dtype,fmt,d,Hkv,G,R", [(BF, "e4m3", 128, 2, 7, 4), (BF, "raw", 64, 1, 6, 3), (BF, "e4m3", 64, 2, 4, 9),
+                                                 (BF, "raw", 128, 1, 28, 2), (F32, "raw", 64, 2, 3, 5), (F32, "e4m3", 128, 1, 9, 1)])
+def test_join_of_many_rows_and_passes(dtype, fmt, d, Hkv, G, R):
+    """Both halves of a history joined, with several rows per sequence and several passes, over units cut into pieces:
+    one attention over all of it, within the bounds of one."""
+    lens, cut = [4000, 64, 90, 33, 7], [1500, 64, 0, 20, 3]
+    B = len(lens)
+    cache, table, g = filled(B, Hkv, d, dtype, fmt, lens, seed=2)
+    q = torch.randn(B, R, G * Hkv, d, generator=g).to(dtype).cuda()
+    head = skv.paged_attn(q, cache, table, i32(cut))
+    out, lse = skv.paged_attn(q, cache, table, i32(lens), first=i32(cut), prior=head)
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    for b in range(B):
+        r = reference(q, cache, table, lens, b)
+        bo, bl = ref.attention_bounds(r, dtype, fmt)
+        # the head's share enters rounded to the dtype: half a step of it, at most of the mass of all keys
+        bo = bo + half * r.mass
+        assert np.all(np.abs(out[b].double().cpu().numpy() - r.out) <= bo)
+        assert np.all(np.abs(lse[b].double().cpu().numpy() - r.lse) <= 2 * bl + 2.0 ** -20)
