@@ -262,9 +262,11 @@ def paged_attn(q: torch.Tensor, cache: TokenCache, page_table: torch.Tensor, len
     """Attention of q [B, R, Hq, d] (the new token's query rows, at position lens - 1; only d must be contiguous)
     over the cached keys at positions max(first, lens - window) .. lens - 1 (first: int32 [B]; window 0: none).
     scale: None for 1 / sqrt(d). softcap c > 0: logits become c tanh(s / c). slopes: fp32 [Hq], s -= slope *
-    distance. prior: (out, lse) of another attention of the same queries, e.g. decode_attn's over the coarsened
-    tokens before `first`; the result is then that of one attention over all keys (out may be prior's out, lse
-    not prior's lse). A row without keys gives out 0, lse -inf. workspace: paged_attn_workspace_bytes bytes of
+    distance. prior: (out, lse) of another attention of the same queries over other keys, joined as it stands: the
+    result is that of one attention over all keys if the prior's logits were scaled, capped and biased alike. So
+    decode_attn's over the coarsened tokens before `first` joins calls without scale, softcap and slopes (it has none
+    of them); a paged_attn over the first n tokens joins any, once slope * (lens - n) is taken off its lse where there
+    are slopes (it counts distances from n - 1). out may be prior's out, lse not prior's lse. A row without keys gives out 0, lse -inf. workspace: paged_attn_workspace_bytes bytes of
     uint8, zeroed once. Returns (out [B, R, Hq, d], lse [B, R, Hq] fp32)."""
     return _scoped(_attn, cache, stream, q, cache, page_table, lens, first, window, scale, softcap, slopes, prior, out,
                    lse, workspace)

@@ -473,9 +473,15 @@ skv_status skv_cache_read(const skv_token_cache *cache, skv_dtype dtype, skv_cac
  *             lens[b] the sequence has no key).
  * slopes    : [Hq] fp32 device: s -= slope * (lens[b] - 1 - j), after the cap.
  * prior_out, prior_lse: another attention of the same queries over other keys, as skv_decode_attn
- *             or this call return it ([B][R][Hq][d] in dtype, [B][R][Hq] fp32): the outputs are then
- *             those of one attention over both sets of keys. prior_out may be out itself; prior_lse may
- *             not overlap lse. A prior_lse of -inf stands for no keys (its prior_out is not read).
+ *             or this call return it ([B][R][Hq][d] in dtype, [B][R][Hq] fp32). The two are joined by
+ *             their partitions as they stand, and neither scale, cap nor bias is applied to the prior:
+ *             the outputs are those of one attention over both sets of keys where the prior's logits
+ *             were scaled, capped and biased alike. skv_decode_attn's are scaled by 1 / sqrt(d), with no cap
+ *             and no bias, so that it makes such a prior only for calls of the default scale without
+ *             softcap and slopes. A prior of this call over the first n tokens counts distances
+ *             from n - 1: lower its lse by slope * (lens[b] - n) first. prior_out may be out itself;
+ *             prior_lse may not overlap lse. A prior_lse of -inf stands for no keys (its prior_out is
+ *             not read).
  * reserved  : must be zero.
  */
 typedef struct {

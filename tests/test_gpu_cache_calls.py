@@ -99,3 +99,28 @@ def test_join_of_many_rows_and_passes(dtype, fmt, d, Hkv, G, R):
         bo = bo + half * r.mass
         assert np.all(np.abs(out[b].double().cpu().numpy() - r.out) <= bo)
         assert np.all(np.abs(lse[b].double().cpu().numpy() - r.lse) <= 2 * bl + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("dtype,fmt,d,G,R", [(BF, "e4m3", 128, 4, 1), (BF, "raw", 64, 3, 4), (F32, "raw", 128, 2, 1)])
+@pytest.mark.parametrize("softcap,scale", [(0.0, None), (5.0, 0.3)])
+def test_join_under_cap_and_bias(dtype, fmt, d, G, R, softcap, scale):
+    """A prior of the same scale, cap and bias joins as documented: its distances counted from its own last token, so that
+    slope * (lens - n) comes off its partition. The result is one attention over all keys."""
+    Hkv, lens, cut = 2, [900, 70, 64, 33], [400, 70, 1, 0]
+    B = len(lens)
+    cache, table, g = filled(B, Hkv, d, dtype, fmt, lens, seed=4)
+    q = torch.randn(B, R, G * Hkv, d, generator=g).to(dtype).cuda()
+    slopes = torch.exp2(-torch.arange(1, G * Hkv + 1).float()).cuda()
+    kw = dict(softcap=softcap, scale=scale, slopes=slopes)
+    head, head_lse = skv.paged_attn(q, cache, table, i32(cut), **kw)
+    head_lse = head_lse - slopes * (i32(lens) - i32(cut))[:, None, None]
+    out, lse = skv.paged_attn(q, cache, table, i32(lens), first=i32(cut), prior=(head, head_lse), **kw)
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    for b in range(B):
+        r = reference(q, cache, table, lens, b, softcap=softcap, scale=scale, slopes=slopes.double().cpu().numpy())
+        bo, bl = ref.attention_bounds(r, dtype, fmt)
+        # the head's share enters rounded to the dtype; its shifted partition is one more fp32 sum of up to |lse| + bias
+        bl = 2 * bl + 2.0 ** -20 + 2.0 ** -22 * float(slopes[0]) * lens[b]
+        bo = bo + half * r.mass + 2 * bl[..., None] * r.mass
+        assert np.all(np.abs(out[b].double().cpu().numpy() - r.out) <= bo)
+        assert np.all(np.abs(lse[b].double().cpu().numpy() - r.lse) <= bl)
