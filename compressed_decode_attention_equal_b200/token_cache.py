@@ -72,7 +72,9 @@ class TokenCache:
             pages = torch.zeros(self.num_pages, self.page_bytes, dtype=torch.uint8, device=device)
         if pages.dtype != torch.uint8 or tuple(pages.shape) != (self.num_pages, self.page_bytes) or not pages.is_contiguous():
             raise ValueError(f"pages must be contiguous uint8 [{self.num_pages}, {self.page_bytes}]")
-        self.pages, self.device, self.on_gpu = pages, pages.device, pages.is_cuda
+        self._pages, self._numel, self.device, self.on_gpu = pages, pages.numel(), pages.device, pages.is_cuda
+        self._struct = _lib.SkvTokenCache(None, self.num_pages)
+        self._ref = ctypes.byref(self._struct)
         p = pages.view(self.num_pages, self.Hkv, CACHE_PAGE_TOKENS // G, group)
         held = torch.float8_e4m3fn if e4m3 else dtype
         shape = (*p.shape[:3], G, self.d)
@@ -80,8 +82,19 @@ class TokenCache:
         self.v = p[..., block:2 * block].view(held).view(shape)
         self.k_exp = p[..., 2 * block:2 * block + G] if e4m3 else None
         self.v_exp = p[..., 2 * block + G:] if e4m3 else None
-        self._struct = _lib.SkvTokenCache(pages.data_ptr(), self.num_pages)
-        self._ref = ctypes.byref(self._struct)
+
+    @property
+    def pages(self) -> torch.Tensor:
+        """The storage that the views and the calls go to: written in place, never another tensor."""
+        return self._pages
+
+    def struct(self):
+        """What the C calls take, by reference, of the pages' address now (their storage may be new)."""
+        t, s = self._pages, self._struct
+        if t.numel() != self._numel or t.device != self.device:
+            raise ValueError("the cache's pages have another size or device than it was made with")
+        s.pages = t.data_ptr()
+        return self._ref
 
     def nbytes(self) -> int:
         return self.pages.numel()
@@ -199,7 +212,7 @@ def _append(k, v, cache, page_table, lens, cu_new, new_lens, workspace):
     kt, kh, _ = k.stride()
     vt, vh, _ = v.stride()
     st = _lib.load().skv_cache_append(k_p, v_p, cache._dtype_code, kt, kh, vt, vh, B, Hkv, d, n, cu_p, cache._format_code,
-                                      cache._ref, table_p, max_pages, lens_p, new_p, ws.data_ptr(), ws.numel(),
+                                      cache.struct(), table_p, max_pages, lens_p, new_p, ws.data_ptr(), ws.numel(),
                                       _stream_handle(device))
     if st:
         raise SkvError(st, "skv_cache_append")
@@ -227,7 +240,7 @@ def _read(cache, page_table, first_list, T_list, k, v, workspace):
         v = torch.empty(rows, dtype=cache.dtype, device=device)
     k_p, v_p = _ptr(k, "k", device, cache.dtype, rows), _ptr(v, "v", device, cache.dtype, rows)
     ws = _workspace(workspace, device, 256)
-    st = _lib.load().skv_cache_read(cache._ref, cache._dtype_code, cache._format_code, B, cache.Hkv, cache.d,
+    st = _lib.load().skv_cache_read(cache.struct(), cache._dtype_code, cache._format_code, B, cache.Hkv, cache.d,
                                     first, T, table_p, max_pages, k_p, v_p, ws.data_ptr(), ws.numel(),
                                     _stream_handle(device))
     if st:
@@ -308,8 +321,8 @@ def _attn(q, cache, page_table, lens, first, window, scale, softcap, slopes, pri
         workspace = torch.zeros(max(size, 256), dtype=torch.uint8, device=device)
     ws = _workspace(workspace, device, 256)
     qb, qr, qh, _ = q.stride()
-    st = _lib.load().skv_paged_attn(q_p, cache._dtype_code, qb, qr, qh, B, R, Hq, cache.Hkv, d, cache._format_code, cache._ref,
-                                    table_p, max_pages, lens_p, out_p, lse_p, ws.data_ptr(), ws.numel(), opts,
+    st = _lib.load().skv_paged_attn(q_p, cache._dtype_code, qb, qr, qh, B, R, Hq, cache.Hkv, d, cache._format_code,
+                                    cache.struct(), table_p, max_pages, lens_p, out_p, lse_p, ws.data_ptr(), ws.numel(), opts,
                                     _stream_handle(device))
     if st:
         raise SkvError(st, "skv_paged_attn")
