@@ -297,11 +297,11 @@ def _attn(q, cache, page_table, lens, first, window, scale, softcap, slopes, pri
     rows = shape[:3]
     opts = None
     if scale is not None or softcap or window or first is not None or slopes is not None or prior is not None:
-        if scale == 0.0:
-            raise ValueError("scale must not be zero")
         if not 0 <= window < 1 << 31:
             raise ValueError("window must be from 0 to 2^31 - 1")
         opts = _lib.SkvPagedAttnOptions(0.0 if scale is None else scale, softcap, window)
+        if opts.scale == 0.0 and scale is not None or opts.softcap == 0.0 and softcap:   # there 0 stands for the defaults
+            raise ValueError("scale and softcap must not be zero in 32 bits")
         if first is not None:
             opts.first = _ptr(first, "first", device, torch.int32, (B,))
         if slopes is not None:

@@ -124,3 +124,15 @@ def test_join_under_cap_and_bias(dtype, fmt, d, G, R, softcap, scale):
         bo = bo + half * r.mass + 2 * bl[..., None] * r.mass
         assert np.all(np.abs(out[b].double().cpu().numpy() - r.out) <= bo)
         assert np.all(np.abs(lse[b].double().cpu().numpy() - r.lse) <= bl)
+
+
+@pytest.mark.parametrize("kw", [dict(scale=0.0), dict(scale=-0.0), dict(scale=1e-46), dict(scale=-1e-50), dict(softcap=1e-46)])
+def test_a_scale_or_cap_that_is_zero_in_32_bits_is_refused(kw):
+    """Zero stands for the defaults below the binding: 1 / sqrt(d) and no cap, the opposite of what was asked for."""
+    cache, table, g = filled(1, 1, 64, BF, "raw", [9])
+    q = torch.randn(1, 1, 1, 64, generator=g).bfloat16().cuda()
+    with pytest.raises(ValueError, match="zero in 32 bits"):
+        skv.paged_attn(q, cache, table, i32([9]), **kw)
+    out, _ = skv.paged_attn(q, cache, table, i32([9]), **{k: math.copysign(1e-44, v) for k, v in kw.items()})
+    (_, v), _ = ref.read_rows(cache, table[0].tolist(), 0, 9)
+    assert np.all(np.abs(out[0, 0, 0].double().cpu().numpy() - v.mean(0)[0]) <= 2.0 ** -8 * np.abs(v).mean(0)[0] + 2.0 ** -14)
