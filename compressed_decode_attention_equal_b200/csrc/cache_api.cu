@@ -42,9 +42,9 @@ skv_status check_pool(const skv_token_cache *c, int Hkv) {
 // Vectors are read 16 bytes at a time. A dimension of one element has no stride that matters.
 bool stride_ok(int64_t stride, int64_t n, int64_t elem) { return stride >= 0 && (n <= 1 || stride * elem % 16 == 0); }
 
-bool overlap(const void *a, const void *b, size_t bytes) {
+bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + bytes && y < x + bytes;
+    return x < y + b_bytes && y < x + a_bytes;
 }
 
 skv_status plan_paged(int dtype, int B, int R, int Hq, int Hkv, int d, int max_pages, PagedArgs *a, size_t *total) {
@@ -99,8 +99,11 @@ skv_status skv_cache_append(const void *k, const void *v, skv_dtype dtype, int64
         return SKV_ERR_INVALID_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(new_lens, 4))
         return SKV_ERR_INVALID_ARG;
-    // new_lens may be lens itself, and nothing in between
-    if (new_lens != lens && overlap(new_lens, lens, static_cast<size_t>(B) * 4)) return SKV_ERR_INVALID_ARG;
+    // new_lens may be lens itself, and nothing in between; nor may it lie in what is read beside it
+    const size_t n4 = static_cast<size_t>(B) * 4;
+    if ((new_lens != lens && overlap(new_lens, n4, lens, n4)) || (cu_new && overlap(new_lens, n4, cu_new, n4 + 4)) ||
+        overlap(new_lens, n4, page_table, n4 * max_pages))
+        return SKV_ERR_INVALID_ARG;
     if (static_cast<int64_t>(n_tokens) * Hkv > INT32_MAX) return SKV_ERR_UNSUPPORTED;
     if (!workspace || !aligned(workspace, 256) || ws_bytes < kWsHeader) return SKV_ERR_WORKSPACE;
     AppendArgs a{};
@@ -147,7 +150,8 @@ skv_status skv_cache_read(const skv_token_cache *cache, skv_dtype dtype, skv_cac
         if (T > 0) items += ((first + T + kGroupTokens - 1) / kGroupTokens - first / kGroupTokens) * Hkv;
         if (items > INT32_MAX) return SKV_ERR_UNSUPPORTED;
     }
-    if (rows > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16))) return SKV_ERR_INVALID_ARG;
+    const size_t bytes = static_cast<size_t>(rows) * d * (dtype == SKV_BF16 ? 2 : 4);
+    if (rows > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16) || overlap(k, bytes, v, bytes))) return SKV_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) || ws_bytes < kWsHeader) return SKV_ERR_WORKSPACE;
     ReadArgs a{};
     a.B = B;
@@ -192,6 +196,8 @@ skv_status skv_paged_attn(const void *q, skv_dtype dtype, int64_t q_seq_stride, 
         return SKV_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(lens, 4))
         return SKV_ERR_INVALID_ARG;
+    const size_t n = static_cast<size_t>(B) * R * Hq;
+    if (overlap(out, n * d * elem, lse, n * 4)) return SKV_ERR_INVALID_ARG;
     a.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
     if (options) {
         for (int i = 0; i < 4; ++i)
@@ -203,10 +209,10 @@ skv_status skv_paged_attn(const void *q, skv_dtype dtype, int64_t q_seq_stride, 
         if (!aligned(options->first, 4) || !aligned(options->slopes, 4) || !aligned(options->prior_out, 16) ||
             !aligned(options->prior_lse, 4))
             return SKV_ERR_INVALID_ARG;
-        const size_t n = static_cast<size_t>(B) * R * Hq;
         // the outputs may replace the prior's; its partitions are read by several threads, so that they may not
-        if (options->prior_out && ((options->prior_out != out && overlap(options->prior_out, out, n * d * elem)) ||
-                                   overlap(options->prior_lse, lse, n * 4)))
+        if (options->prior_out && ((options->prior_out != out && overlap(options->prior_out, n * d * elem, out, n * d * elem)) ||
+                                   overlap(options->prior_lse, n * 4, lse, n * 4) ||
+                                   overlap(options->prior_lse, n * 4, out, n * d * elem)))
             return SKV_ERR_INVALID_ARG;
         if (options->scale != 0.f) a.scale = options->scale;
         a.softcap = options->softcap;

@@ -438,7 +438,8 @@ size_t skv_cache_page_bytes(skv_dtype dtype, skv_cache_format format, int Hkv, i
  *             sequence gets n_tokens / B tokens (n_tokens a multiple of B).
  * lens      : [B] int32 device, tokens held before: new token i goes to position lens[b] + i, whose
  *             page the page table must already name.
- * new_lens  : [B] int32 device output, lens + the new tokens. May be lens itself (updated in place).
+ * new_lens  : [B] int32 device output, lens + the new tokens. May be lens itself (updated in place), and may
+ *             overlap neither it otherwise nor cu_new or the page table.
  * workspace : >= 256 bytes, zero-filled before its first use: error flags and a counter that every
  *             call returns to zero.
  * One launch, graph-capturable. Device-detected, the offending tokens skipped: a page id outside the
@@ -457,8 +458,8 @@ skv_status skv_cache_append(const void *k, const void *v, skv_dtype dtype, int64
  * Read positions [first_b, first_b + T_b) of every sequence back into the packed layout that
  * skv_coarsen takes: sequence b a contiguous [Hkv][T_b][d] block of k and v in dtype.
  * first_host, T_host: [B] host (first_b + T_b <= max_pages * 64; the positions must have been
- * appended). A page id outside the cache gives zeros and sets the device flag. workspace: >= 256
- * bytes (error flags). Errors as skv_cache_append.
+ * appended). k and v may not overlap. A page id outside the cache gives zeros and sets the device flag.
+ * workspace: >= 256 bytes (error flags). Errors as skv_cache_append.
  */
 skv_status skv_cache_read(const skv_token_cache *cache, skv_dtype dtype, skv_cache_format format, int B, int Hkv, int d,
                           const int32_t *first_host, const int32_t *T_host, const int32_t *page_table, int max_pages,
@@ -480,7 +481,7 @@ skv_status skv_cache_read(const skv_token_cache *cache, skv_dtype dtype, skv_cac
  *             and no bias, so that it makes such a prior only for calls of the default scale without
  *             softcap and slopes. A prior of this call over the first n tokens counts distances
  *             from n - 1: lower its lse by slope * (lens[b] - n) first. prior_out may be out itself;
- *             prior_lse may not overlap lse. A prior_lse of -inf stands for no keys (its prior_out is
+ *             prior_lse may overlap neither lse nor out. A prior_lse of -inf stands for no keys (its prior_out is
  *             not read).
  * reserved  : must be zero.
  */
@@ -508,7 +509,8 @@ size_t skv_paged_attn_workspace_bytes(int B, int R, int Hq, int Hkv, int d, int 
  *         and sees every key there is. Query head hq reads KV head hq / (Hq / Hkv).
  * s_j = scale q.k_j (capped, biased) over the keys j in [max(first, lens - window), lens);
  * out = softmax(s) V ([B][R][Hq][d] in dtype), lse = ln sum exp(s_j) ([B][R][Hq] fp32). A row that
- * sees no key gives out = 0, lse = -inf (joined with a prior: the prior). NaN in a key or value that
+ * sees no key gives out = 0, lse = -inf (joined with a prior: the prior). out and lse may not overlap, and out not q
+ * unless it is q itself and q is contiguous. NaN in a key or value that
  * is seen gives NaN; what is not seen never enters.
  * workspace : skv_paged_attn_workspace_bytes bytes, 256-byte aligned, zero-filled before its first use.
  * The keys are split over the whole GPU and joined in a fixed order: equal inputs give equal bits.

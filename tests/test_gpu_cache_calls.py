@@ -136,3 +136,14 @@ def test_a_scale_or_cap_that_is_zero_in_32_bits_is_refused(kw):
     out, _ = skv.paged_attn(q, cache, table, i32([9]), **{k: math.copysign(1e-44, v) for k, v in kw.items()})
     (_, v), _ = ref.read_rows(cache, table[0].tolist(), 0, 9)
     assert np.all(np.abs(out[0, 0, 0].double().cpu().numpy() - v.mean(0)[0]) <= 2.0 ** -8 * np.abs(v).mean(0)[0] + 2.0 ** -14)
+
+
+@pytest.mark.parametrize("dtype,fmt,d,G,R", [(BF, "e4m3", 128, 7, 1), (BF, "raw", 64, 9, 5), (F32, "raw", 128, 3, 4)])
+def test_the_outputs_may_take_the_queries_place(dtype, fmt, d, G, R):
+    """out = q, with units that are cut into pieces, several passes and short units among them."""
+    Hkv, lens = 2, [9000, 0, 3, 700, 64]
+    cache, table, g = filled(5, Hkv, d, dtype, fmt, lens, seed=7)
+    q = torch.randn(5, R, G * Hkv, d, generator=g).to(dtype).cuda()
+    want = skv.paged_attn(q, cache, table, i32(lens))
+    out, lse = skv.paged_attn(q, cache, table, i32(lens), out=q)
+    assert out is q and torch.equal(out, want[0]) and torch.equal(lse, want[1])
