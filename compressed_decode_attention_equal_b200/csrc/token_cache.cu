@@ -22,7 +22,9 @@ namespace {
 constexpr int kAppendWarps = 4;
 constexpr int kHeads = 4;          // independent loads in flight per lane
 constexpr int kLaneElems = 8;
-constexpr int kAppendTokens = 4;   // most steps of a warp: 2, 4, 8, 16 measured 51.5, 43.7, 45.8, 53.3 us (74,211 tokens x 4 heads)
+// most steps of a warp: 2, 4, 8, 16 measured 51.5, 43.7, 45.8, 53.3 us (74,211 tokens x 4 heads). A lane looks up one
+// place, so that a warp's tokens (its rows, in the flat form, 8 to a step at d = 64) are 32 at most.
+constexpr int kAppendTokens = 4;
 
 // two fp32 to two e4m3 codes (round to nearest even, saturating; lo in the low byte)
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
@@ -159,6 +161,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_c
     constexpr int N = kLaneElems, W = N * static_cast<int>(sizeof(T)) / 4;
     constexpr int LANES = D / N, SUBS = 32 / (2 * LANES);   // lanes of a vector, rows side by side
     constexpr int ROWS = kHeads * SUBS;                     // rows of a step
+    static_assert(kAppendTokens * (FLAT ? ROWS : 1) <= 32, "a lane per place");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, sub = lane / (2 * LANES), half = lane / LANES & 1, l = lane % LANES;
@@ -443,7 +446,7 @@ cudaError_t append_d(const AppendArgs &a0, cudaStream_t s) {
     constexpr int ROWS = kHeads * (128 / D);   // rows of a step
     const bool flat = a.Hkv % ROWS != 0;
     const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.Hkv, all = (rows + ROWS - 1) / ROWS;   // steps
-    // steps of a warp: one while there are not enough warps for the GPU
+    // steps of a warp: one while there are not enough warps for the GPU (148 SMs, 32 warps each)
     const int64_t per = all / (148 * 32);
     a.per_warp = static_cast<int>(per < 1 ? 1 : per > kAppendTokens ? kAppendTokens : per);
     const int64_t items = flat ? (all + a.per_warp - 1) / a.per_warp
