@@ -279,8 +279,10 @@ def paged_attn(q: torch.Tensor, cache: TokenCache, page_table: torch.Tensor, len
     result is that of one attention over all keys if the prior's logits were scaled, capped and biased alike. So
     decode_attn's over the coarsened tokens before `first` joins calls without scale, softcap and slopes (it has none
     of them); a paged_attn over the first n tokens joins any, once slope * (lens - n) is taken off its lse where there
-    are slopes (it counts distances from n - 1). out may be prior's out, lse not prior's lse. A row without keys gives out 0, lse -inf. workspace: paged_attn_workspace_bytes bytes of
-    uint8, zeroed once. Returns (out [B, R, Hq, d], lse [B, R, Hq] fp32)."""
+    are slopes (it counts distances from n - 1). out may be prior's out, or q itself where q is contiguous; lse not
+    prior's lse. A row without keys gives out 0, lse -inf. workspace: paged_attn_workspace_bytes bytes of uint8, zeroed
+    once; the cache's calls may share it, ordered on one stream, but coarsen, the streaming calls and decode_attn may
+    not, whose scratch lies where its counters are. Returns (out [B, R, Hq, d], lse [B, R, Hq] fp32)."""
     return _scoped(_attn, cache, stream, q, cache, page_table, lens, first, window, scale, softcap, slopes, prior, out,
                    lse, workspace)
 

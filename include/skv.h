@@ -497,7 +497,8 @@ typedef struct {
 } skv_paged_attn_options;
 
 /* Bytes of device workspace skv_paged_attn needs (0 on invalid arguments). Calls of any shape that
- * need no more may share it (not with skv_decode_attn), ordered on one stream. */
+ * need no more may share it, with skv_cache_append and skv_cache_read too, ordered on one stream; other entry
+ * points may not, whose scratch lies where its counters are. */
 size_t skv_paged_attn_workspace_bytes(int B, int R, int Hq, int Hkv, int d, int max_pages);
 
 /*
