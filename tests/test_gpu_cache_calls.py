@@ -147,3 +147,68 @@ def test_the_outputs_may_take_the_queries_place(dtype, fmt, d, G, R):
     want = skv.paged_attn(q, cache, table, i32(lens))
     out, lse = skv.paged_attn(q, cache, table, i32(lens), out=q)
     assert out is q and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype,fmt,d,G", [(BF, "e4m3", 64, 7), (BF, "raw", 128, 12), (F32, "e4m3", 128, 2)])
+def test_positions_at_the_end_of_the_range(dtype, fmt, d, G):
+    """A sequence of 2^30 tokens, the most there may be, of which the last few hundred are appended, read and attended to
+    through a start or a window: the bits of the same tokens at the same places of a short sequence."""
+    Hkv, n, T = 2, 300, 1 << 30
+    g = torch.Generator().manual_seed(d)
+    x = rand(g, 2 * n, Hkv, d, dtype=dtype).cuda()
+    q = torch.randn(1, 1, G * Hkv, d, generator=g).to(dtype).cuda()
+    slopes = torch.exp2(-torch.arange(1, G * Hkv + 1).float()).cuda()
+    skip = -n % 64                                          # both runs start at the same place of a page
+    small, table = make(1, Hkv, d, dtype, fmt, [skip + n])
+    far = torch.full((1, T // 64), -1, dtype=torch.int32, device="cuda")
+    far[:, -table.shape[1]:] = table
+    got = []
+    for end, tab in ((skip + n, table), (T, far)):
+        small.pages.fill_(255)
+        ws = torch.zeros(skv.paged_attn_workspace_bytes(1, 1, G * Hkv, Hkv, d, tab.shape[1]), dtype=torch.uint8, device="cuda")
+        lens = skv.cache_append(x[:n], x[n:], small, tab, i32([end - n]), workspace=ws)
+        assert lens.tolist() == [end]
+        read = skv.cache_read(small, tab, [end - n], [n], workspace=ws)
+        a = skv.paged_attn(q, small, tab, lens, first=i32([end - n]), slopes=slopes, workspace=ws)
+        b = skv.paged_attn(q, small, tab, lens, window=n, slopes=slopes, workspace=ws)
+        ok(ws)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        got.append((*read, *a))
+    for u, w in zip(*got):
+        assert torch.equal(u, w)
+    with pytest.raises(skv.SkvError):
+        skv.cache_read(small, far, [T - 1], [2])
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    assert skv.cache_append(x[:1], x[:1], small, far, i32([T]), workspace=ws).tolist() == [T]
+    assert skv.workspace_error(ws) == (_lib.SKV_ERR_DEVICE, _lib.FLAG_BAD_LENS)
+
+
+def test_two_captured_graphs_share_a_workspace():
+    """Calls of different shapes captured into two graphs over one workspace and replayed in turns, eager calls between."""
+    g = torch.Generator().manual_seed(12)
+    calls = []
+    for B, Hkv, G, R, d, dtype, fmt, n in ((1, 2, 7, 4, 128, BF, "e4m3", 20000), (40, 3, 1, 1, 64, F32, "raw", 500), (2, 8, 2, 1, 128, BF, "raw", 3000)):
+        cache, table, _ = filled(B, Hkv, d, dtype, fmt, [n - b for b in range(B)], seed=n)
+        q = torch.randn(B, R, G * Hkv, d, generator=g).to(dtype).cuda()
+        calls.append((q, cache, table, i32([n - b for b in range(B)])))
+    size = max(skv.paged_attn_workspace_bytes(q.shape[0], q.shape[1], q.shape[2], c.Hkv, c.d, t.shape[1]) for q, c, t, _ in calls)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = [skv.paged_attn(*c) for c in calls]
+    graphs = []
+    torch.cuda.synchronize()
+    for order in ((0, 1, 2), (2, 0)):
+        graph, outs = torch.cuda.CUDAGraph(), []
+        with torch.cuda.graph(graph):
+            for i in order:
+                outs.append((i, *skv.paged_attn(*calls[i], workspace=ws)))
+        graphs.append((graph, outs))
+    for turn in range(6):
+        graph, outs = graphs[turn % 2]
+        for _, o, l in outs:
+            o.fill_(math.nan), l.fill_(math.nan)
+        graph.replay()
+        o, l = skv.paged_attn(*calls[turn % 3], workspace=ws)
+        assert torch.equal(o, want[turn % 3][0]) and torch.equal(l, want[turn % 3][1])
+        for i, o, l in outs:
+            assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]), (turn, i)
+    ok(ws)
