@@ -72,8 +72,8 @@ class TokenCache:
             pages = torch.zeros(self.num_pages, self.page_bytes, dtype=torch.uint8, device=device)
         if pages.dtype != torch.uint8 or tuple(pages.shape) != (self.num_pages, self.page_bytes) or not pages.is_contiguous():
             raise ValueError(f"pages must be contiguous uint8 [{self.num_pages}, {self.page_bytes}]")
-        self._pages, self._numel, self.device, self.on_gpu = pages, pages.numel(), pages.device, pages.is_cuda
-        self._struct = _lib.SkvTokenCache(None, self.num_pages)
+        self._pages, self._at, self.device, self.on_gpu = pages, pages.data_ptr(), pages.device, pages.is_cuda
+        self._struct = _lib.SkvTokenCache(self._at, self.num_pages)
         self._ref = ctypes.byref(self._struct)
         p = pages.view(self.num_pages, self.Hkv, CACHE_PAGE_TOKENS // G, group)
         held = torch.float8_e4m3fn if e4m3 else dtype
@@ -90,14 +90,15 @@ class TokenCache:
 
     def struct(self):
         """What the C calls take, by reference, of the pages' address now (their storage may be new)."""
-        t, s = self._pages, self._struct
-        if t.numel() != self._numel or t.device != self.device:
-            raise ValueError("the cache's pages have another size or device than it was made with")
-        s.pages = t.data_ptr()
+        at = self._pages.data_ptr()
+        if at != self._at:
+            if self._pages.numel() != self.nbytes() or self._pages.device != self.device:
+                raise ValueError("the cache's pages have another size or device than it was made with")
+            self._struct.pages = self._at = at
         return self._ref
 
     def nbytes(self) -> int:
-        return self.pages.numel()
+        return self.num_pages * self.page_bytes
 
 
 # ---------------------------------------------------------------------------
