@@ -240,8 +240,8 @@ struct GroupRing {
 //   79.9 and 51.9 us with one or two; 28 rows over 8 x 4 x 16,384 keys 63.6 -> 70.3 us). Sums and maxima are fp32. A
 //   reference maximum moves only when it is exceeded by 8 (2^8), so that the rescale of O runs rarely.
 // Measured: 32 sequences x 4 heads x 32,768 e4m3 keys at 7 rows take 174 us, 96% of the copy rate (raw, ragged:
-// 79.5 us, 94%). An mma.sync, a conversion and an FMA add up on one scheduler here instead of overlapping, so
-// that many rows are bound by the instruction rate: 28 rows over 8 x 4 x 16,384 e4m3 keys take 62.5 us, 34%.
+// 80 us, 93%). An mma.sync, a conversion and an FMA add up on one scheduler here instead of overlapping, so
+// that many rows are bound by the instruction rate: 28 rows over 8 x 4 x 16,384 e4m3 keys take 60.8 us, 34%.
 template <bool E4M3, int D, int NT, int W, int S, int CTAS, int TP>
 __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
     using Sm = MmaSmem<E4M3, D, NT, W, S, CTAS, TP>;
@@ -346,7 +346,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
             const int d0 = E4M3 ? 64 * (ks / 4) + 16 * tq + 4 * (ks % 4) : 32 * (ks / 2) + 8 * tq + 4 * (ks % 2);
             return *reinterpret_cast<const uint2 *>(sm.q[8 * nt + g] + 2 * d0);
         };
-        constexpr bool QREG = NT <= 2;   // the queries stay in registers (16 rows: 43.1 -> 41.1 us; 28 would spill)
+        // The queries stay in registers (16 rows: 43.1 -> 41.1 us). Four tiles of rows have none left for them: at d = 128
+        // they spill 64 bytes (e4m3) and 108 (raw) without; with, 61 -> 71 us.
+        constexpr bool QREG = NT <= 2;
         uint2 qf[QREG ? NT : 1][QREG ? KS : 1];
         if constexpr (QREG) {
 #pragma unroll
@@ -1066,7 +1068,7 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     constexpr int TP = D == 64 ? 2 : 1;
     // Warps and CTAs per SM. e4m3, 8 rows: two CTAs of 8 warps at 128 registers (7B batch 174 us; one CTA of 8 warps
     // 188 us: too few to hide a tile's latency). Raw tiles are twice the bytes for the same work: one CTA of 8
-    // warps (79.4 us; two of 4 84.2). More rows need the registers: 16 and 28 rows 41.1 and 62.5 us; with three
+    // warps (80 us; two of 4 84.2). More rows need the registers: 16 and 28 rows 41.6 and 60.8 us; with three
     // and two CTAs of 4 warps 55.8 and 75.2.
     if constexpr (E4M3) {
         if (a.pass_rows == 8) return launch_mma<E4M3, D, 1, 8, 2, 2, TP>(a, s);

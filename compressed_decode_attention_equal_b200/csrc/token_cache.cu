@@ -16,7 +16,7 @@ namespace {
 // append: a vector is 8 elements per lane, so that a warp takes the key and value of one row (d = 128) or two
 // (d = 64) at once, kHeads times that per step; the next step's loads are in flight while one is quantised, and
 // the lanes look the tokens' pages up side by side. The instruction rate bounds it for long prompts (74,211 tokens
-// x 4 heads of bf16 to e4m3: 40.1 us, 88% of the copy rate; without the limit of 64 registers 48): one round of
+// x 4 heads of bf16 to e4m3: 40.5 us, 87% of the copy rate; without the limit of 64 registers 48): one round of
 // page lookups per warp, bf16 maxima of two vectors in one word and packed products keep it there.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
@@ -153,7 +153,7 @@ __device__ __forceinline__ void quantise(const uint32_t (&w)[W], int e, uint32_t
 }
 
 // FLAT false: a step is that many heads of one token. FLAT true: as many consecutive (token, head) rows, whatever
-// their tokens; for head counts that do not fill steps (74,211 tokens x 1 head 26.0 us instead of 56.8; 4 heads
+// their tokens; for head counts that do not fill steps (74,211 tokens x 1 head 26.4 us instead of 56.8; 4 heads
 // would take 44.6 instead of 40.1 with a lookup per row).
 template <typename T, bool E4M3, int D, bool FLAT>
 __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(T) == 2 ? 8 : 4) k_cache_append(const AppendArgs a) {
