@@ -16,7 +16,6 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kSlack = 8.f;                  // 2^8 times a value's scale, 2^119 at most, stays within fp32
 constexpr float kRaise = 7.f;                  // a weight is at most 2^(kSlack + kRaise), half of what fp16 holds
 constexpr float kSpan = 126.f;                 // 2^126 stays finite, and 2^-126 is the smallest normal output
-constexpr float kLeast = 1.17549435e-38f;      // 2^-126, the smallest normal number
 constexpr float kNoLogit = -3.402823466e38f;   // no maximum yet: finite, so that a masked logit (-inf) less it is not NaN
 
 // log2(e) c tanh(x / c), relative to itself 2^-20 or better for every c: up to |x / c| = 1/4 x times the series of
@@ -543,11 +542,11 @@ __global__ void __launch_bounds__(32 * W, CTAS) k_paged_mma(const PagedArgs a) {
                             const float x = p[2 * c], y = p[2 * c + 1];
                             if constexpr (E4M3) {
                                 pb[nt][c] = movmatrix_t(pack_f16x2(x, y));
-                            } else {   // upper halves, and what they leave (never 0: an infinite value stays one)
+                            } else {   // upper halves, and what they leave: 2^-24 at least, not 0, which would make an infinite value NaN
                                 const uint32_t u = __float_as_uint(x), w = __float_as_uint(y);
                                 pb[nt][c] = movmatrix_t(__byte_perm(u, w, 0x7632));
-                                pr[nt][c] = movmatrix_t(pack_bf16x2(fmaxf(x - __uint_as_float(u & 0xffff0000u), kLeast),
-                                                                    fmaxf(y - __uint_as_float(w & 0xffff0000u), kLeast)));
+                                pr[nt][c] = movmatrix_t(pack_bf16x2(fmaxf(x - __uint_as_float(u & 0xffff0000u), x * 0x1p-24f),
+                                                                    fmaxf(y - __uint_as_float(w & 0xffff0000u), y * 0x1p-24f)));
                             }
                         }
                     }

@@ -102,3 +102,21 @@ def test_caps_of_every_size(dtype, fmt, cap, d, G):
     top = np.abs(x[0] @ kk[:, 0].T).max(-1) / math.sqrt(d)
     r.dlogit = ref.Attn(x, kk, vv, vs, n - 1, 0).dlogit + 2.0 ** -20 * np.minimum(cap, top)
     ref.check_attention(out[0], lse[0], r, dtype, fmt, f"cap {cap}")
+
+
+@pytest.mark.parametrize("dtype,fmt", [(BF, "raw"), (BF, "e4m3"), (F32, "raw")])
+@pytest.mark.parametrize("d,G", [(128, 7), (64, 12), (128, 28)])
+def test_a_weight_of_zero_takes_nothing_of_a_huge_value(dtype, fmt, d, G):
+    """Keys so far below the others that their weights are zero in 32 bits, with values of 2^120: the output is that of the
+    others, whatever the weights are made of. (In 64 bits the huge ones add e^-400 2^120, nothing.)"""
+    n = 90
+    g = torch.Generator().manual_seed(G)
+    k, v = torch.randn(n, 1, d, generator=g) / 64, torch.randn(n, 1, d, generator=g)
+    k[1::2] -= 400 / math.sqrt(d)                            # q of ones: logits of about 0 and -400
+    v[1::2] = 2.0 ** 120
+    cache, table = put(k, v, dtype, fmt)
+    q = torch.ones(1, 1, G, d).to(dtype).cuda()
+    out, lse = skv.paged_attn(q, cache, table, i32([n]))
+    r = reference(q, cache, table, [n], 0)
+    r.tiny = r.tiny * 0                                     # that term takes a weight's scale from its value's
+    ref.check_attention(out[0], lse[0], r, dtype, fmt)
