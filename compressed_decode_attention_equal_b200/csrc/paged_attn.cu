@@ -233,10 +233,10 @@ struct GroupRing {
 //   So neither a value's scale nor a value of zeros can take precision from the partition or the other values.
 //   Weights are 16-bit operands of the second product, the partition keeps them in fp32. e4m3 caches: one fp16 number
 //   (2^-11 relative), far below what the codes themselves hold; the 7 put the largest near fp16's top, so that its
-//   smallest steps, 2^-24, are 2^-31 of it: 2^19 keys, a warp's most of one sequence, lose 2^-13 by them. Raw caches
+//   smallest steps, 2^-24, are 2^-31 of it: 2^19 keys, a warp's share of a full memory, lose 2^-13 by them. Raw caches
 //   hold values whole, so that a weight of one bf16 number (2^-8) would be their largest error: it is two, its upper
 //   half and the rest (2^-16), for twice the second product's instructions (up to 16 rows in the shadow of the copies:
-//   79.9 and 51.9 us with one or two; 28 rows over 8 x 4 x 16,384 keys 63.6 -> 70.3 us). Sums and maxima are fp32. A
+//   79.9 and 51.9 us with one or two; 28 rows over 8 x 4 x 16,384 keys 63.1 -> 69.5 us). Sums and maxima are fp32. A
 //   reference maximum moves only when it is exceeded by 8 (2^8), so that the rescale of O runs rarely.
 // Measured: 32 sequences x 4 heads x 32,768 e4m3 keys at 7 rows take 174 us, 96% of the copy rate (raw, ragged:
 // 80 us, 93%). An mma.sync, a conversion and an FMA add up on one scheduler here instead of overlapping, so
